@@ -1,4 +1,5 @@
-"""ctypes declarations of libssd_replay.so (include/ssd_replay.h).
+"""ctypes declarations of libssd_replay.so (include/ssd_replay.h,
+include/ssd_step.h).
 
 Loading fails loudly when the library has not been built: there is no
 fallback implementation.
@@ -26,6 +27,15 @@ EXPORTS = ("ssd_status_string", "ssd_replay_cache_bytes", "ssd_prefill_workspace
            "ssd_replay_page_bytes", "ssd_conv1d_varlen", "ssd_conv1d_update",
            "ssd_replay_verify", "ssd_replay_accept", "ssm_state_update_varlen",
            "ssd_prefill_chunk_count", "ssd_replay_decode_static", "ssd_replay_decode_conv")
+
+# every symbol include/ssd_step.h declares
+STEP_EXPORTS = ("ssd_linear", "ssd_in_proj", "ssd_gated_norm", "ssd_token_logprobs",
+                "ssd_replay_pages_reserve", "ssd_replay_pages_trim", "ssd_replay_cache_free",
+                "ssd_replay_cache_copy", "ssd_replay_pages_compact",
+                "ssd_replay_pages_compact_workspace_bytes")
+
+# ssd_activation
+ACTIVATIONS = {"none": 0, "silu": 1, "gelu": 2, "relu2": 3}
 
 
 class ssd_shape(ctypes.Structure):
@@ -105,6 +115,20 @@ def load() -> ctypes.CDLL:
                                             vp, vp, vp, vp, vp]
     lib.ssm_state_update.restype = ctypes.c_int
     lib.ssm_state_update.argtypes = [shp, i32, i32, vp, vp, vp, vp, vp, vp, vp, vp, vp, vp, vp]
+    f32 = ctypes.c_float
+    lib.ssd_linear.argtypes = [i64, i64, i64, i32, i32, i32, vp, vp, vp, vp, vp, vp]
+    lib.ssd_in_proj.argtypes = [shp, i64, i64, vp, vp, vp, vp, vp, vp, vp]
+    lib.ssd_gated_norm.argtypes = [shp, i64, i32, f32, i32, vp, vp, vp, vp, vp]
+    lib.ssd_token_logprobs.argtypes = [i64, i64, i32, vp, vp, i32, vp, vp, vp, vp, vp, vp]
+    lib.ssd_replay_pages_reserve.argtypes = [shp, cp, i32, vp, vp, vp, i32, vp, vp]
+    lib.ssd_replay_pages_trim.argtypes = [shp, cp, i32, vp, vp]
+    lib.ssd_replay_cache_free.argtypes = [shp, cp, i32, vp, vp]
+    lib.ssd_replay_cache_copy.argtypes = [shp, cp, cp, i32, vp, vp, vp, vp]
+    lib.ssd_replay_pages_compact.argtypes = [shp, cp, vp, vp, sz, vp]
+    for name in STEP_EXPORTS:
+        getattr(lib, name).restype = ctypes.c_int
+    lib.ssd_replay_pages_compact_workspace_bytes.restype = sz
+    lib.ssd_replay_pages_compact_workspace_bytes.argtypes = [cp]
     _lib = lib
     return lib
 

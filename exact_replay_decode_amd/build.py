@@ -23,7 +23,9 @@ PROBE_SOURCE = "ssd_probe.hip"
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 ARCH = "gfx950"
 
-SOURCES = ["ssd_api.cpp", "ssd_scalar.hip", "ssd_mfma.hip", "ssd_conv.hip", "ssd_scratch.hip"]
+SOURCES = ["ssd_api.cpp", "ssd_scalar.hip", "ssd_mfma.hip", "ssd_conv.hip", "ssd_scratch.hip",
+           "ssd_step_api.cpp", "ssd_linear.hip", "ssd_norm.hip", "ssd_logprobs.hip",
+           "ssd_pages.hip"]
 DEVICE_FLAGS = ["-Xclang", "-target-feature", "-Xclang", "-packed-fp32-ops",
                 "-mllvm", "-amdgpu-mfma-vgpr-form"]
 

@@ -1,0 +1,101 @@
+// ssd_step.hpp -- argument blocks and launchers of the operators around the
+// scan (include/ssd_step.h). Host-side only types; pointers are device
+// pointers.
+#pragma once
+
+#include <stdint.h>
+
+#include <hip/hip_runtime_api.h>
+
+#include "ssd_internal.hpp"
+
+namespace ssd {
+
+// Columns [n0, n1) of a product's output go to p [M, n1 - n0]. n0 is a
+// multiple of 16, so a 16-column tile has one destination.
+struct LinearSeg {
+    void *p;
+    int32_t n0, n1;
+    int32_t bf16;
+};
+
+struct LinearArgs {
+    int32_t M, N, K;
+    int32_t io_bf16;
+    int32_t act;              // ssd_activation
+    const void *x, *w;        // [M,K], [N,K]
+    const float *bias;        // [N] or null
+    const void *residual;     // [M,N] or null (one segment only)
+    int32_t nseg;
+    LinearSeg seg[3];
+};
+
+struct NormArgs {
+    int64_t T;
+    int32_t C, gs;            // channels of a row, channels of a group
+    int32_t io_bf16, before;
+    float eps;
+    const void *y, *z;        // z may be null
+    const float *w;
+    void *out;
+};
+
+struct LogprobArgs {
+    int64_t T;
+    int32_t V, bf16, k;
+    const void *logits;
+    const int32_t *tokens;
+    float *logprob, *entropy;  // entropy, rank may be null
+    int32_t *rank;
+    int32_t *top_ids;
+    float *top_logprobs;
+};
+
+// A cache as the page kernels see it.
+struct SlotMap {
+    int32_t *pages;           // [slots, npp] or null
+    int32_t npp, shift, num_pages, num_slots;
+    int32_t Q;
+    int32_t *buf_len;
+    int64_t *boundary_pos;
+    float *state;
+    void *state_bf;
+    void *buf_x, *buf_dt, *buf_B, *buf_C;
+};
+
+struct ReserveArgs {
+    SlotMap c;
+    int32_t n;
+    const int32_t *slot_idx, *like_idx, *tokens;
+    int32_t tokens_all;
+    int32_t *granted;
+};
+
+// Bytes of one token's row in each buffer, and of one slot's state.
+struct RowBytes {
+    int32_t x, dt, bc;        // bc: B, and C alike
+    int64_t state;            // fp32; the bf16 copy has half
+};
+
+struct CopyArgs {
+    SlotMap dst, src;
+    RowBytes r;
+    int32_t n;
+    const int32_t *dst_idx, *src_idx;
+    int32_t *copied;
+};
+
+hipError_t launch_linear(const LinearArgs &a, hipStream_t stream);
+hipError_t launch_gated_norm(const NormArgs &a, hipStream_t stream);
+hipError_t launch_logprobs(const LogprobArgs &a, hipStream_t stream);
+hipError_t launch_pages_reserve(const ReserveArgs &a, hipStream_t stream);
+hipError_t launch_pages_trim(const SlotMap &c, int32_t n, const int32_t *slot_idx,
+                             hipStream_t stream);
+hipError_t launch_cache_free(const SlotMap &c, const RowBytes &r, int32_t n,
+                             const int32_t *slot_idx, hipStream_t stream);
+hipError_t launch_cache_copy(const CopyArgs &a, hipStream_t stream);
+// work: int32 [2 + num_pages] (move count, then from/to pairs)
+hipError_t launch_pages_compact(const SlotMap &c, const RowBytes &r, int32_t *used, int32_t *work,
+                                hipStream_t stream);
+
+}  // namespace ssd
