@@ -379,7 +379,8 @@ def run(state):
 def _own(s, c, op):
     erd = s["erd"]
     if op == "in_proj":
-        return erd.ssd_in_proj(s["shape"], s["x"], s["w"])
+        z, xBC, dt = erd.ssd_in_proj(s["shape"], s["x"], s["w"])
+        return z.view(c["M"], -1), xBC, dt
     if op == "linear":
         return erd.ssd_linear(s["x"], s["w"], bias=s["bias"], activation=c["act"],
                               residual=s["residual"], out_dtype=DT[c["out"]])
