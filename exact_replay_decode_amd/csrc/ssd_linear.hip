@@ -3,16 +3,24 @@
 //   out[m][n] = act(sum_k x[m][k] w[n][k] + bias[n]) + residual[m][n]
 //
 // Every output is one fp32 accumulation chain of matrix-core instructions over
-// k ascending from zero: v_mfma_f32_16x16x32_bf16 (32 k a step) or
-// v_mfma_f32_16x16x4_f32 (4 k a step), k past K filled with zeros on both
-// sides. An MFMA result element depends on its own row, its own column and
-// its accumulator only, so every kernel here that walks k in this order
-// gives the same bits whatever its tile shape, and a row's bits do not
-// depend on the number of rows. (The price is that k is never split over
-// waves that would add partial sums.)
+// 64-byte steps of k, ascending from zero: one v_mfma_f32_16x16x32_bf16 for the
+// step's 32 k in bf16, four v_mfma_f32_16x16x4_f32 for its 16 k in fp32 (the
+// i-th takes k = i, 4 + i, 8 + i, 12 + i of the step); k past K are zeros on
+// both sides. An MFMA result element depends on its own row, its own column
+// and its accumulator only, so every tile shape here gives the same bits, and
+// a row's bits do not depend on the number of rows. (The price is that k is
+// never split over waves that would add partial sums.)
 //
 // The instruction's rows are output columns n and its columns are rows m of x:
-// a lane then holds four consecutive n of one row, which it stores together.
+// a lane then holds four consecutive n of one row.
+//
+// What bounds it, measured with copies that leave parts out: at 8192^3 the matrix
+// instructions and LDS reads alone take 784 us, the loads alone 703 us, together
+// 950 us (1160 TFLOP/s; the library's product on the same card 764 us); the
+// LDS serves both, 1.5 KB read per MFMA of a 64 x 128 wave tile. At 256 x 2048 x 4096
+// (one 64 x 32 tile per compute unit, one wave per SIMD) 10 us of loads and 12 us
+// of reads and MFMAs give 15 us: latency. A single row streams w: 16 columns a
+// workgroup, every load of the row in flight at once.
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
@@ -47,118 +55,461 @@ __device__ __forceinline__ float activate(float v, int act) {
     }
 }
 
-// Lane l of a 16 x 16 tile holds row m = l % 16, columns n = 4 (l / 16) + i:
-// bias, activation, residual, one rounding, stored. n0, m0: the tile's first
-// column (a multiple of 16) and row.
-__device__ __forceinline__ void store_tile(const LinearArgs &a, int m0, int n0, const f32x4 &acc) {
-    const int lane = threadIdx.x & 63;
-    const int m = m0 + (lane & 15), n = n0 + 4 * (lane >> 4);
-    if (m >= a.M || n >= a.N)
-        return;
+// Columns n .. n + 7 of row m, n a multiple of 8: bias, activation, residual, one
+// rounding, 16-byte accesses where the eight are all there (of any alignment:
+// N may be odd).
+__device__ __forceinline__ void store_eight(const LinearArgs &a, int m, int n, float (&v)[8]) {
+    typedef f32x4 f32x4_u __attribute__((aligned(4)));
+    typedef u32x4 u32x4_u __attribute__((aligned(2)));
     LinearSeg s = a.seg[0];
-    if (a.nseg > 1 && n0 >= s.n1)
-        s = n0 >= a.seg[1].n1 ? a.seg[2] : a.seg[1];
+    if (a.nseg > 1 && n >= s.n1)
+        s = n >= a.seg[1].n1 ? a.seg[2] : a.seg[1];
     const int64_t at = (int64_t)m * (s.n1 - s.n0) + (n - s.n0);
-    const int cnt = min(4, a.N - n);
+    const int cnt = a.N - n;
+    float r[8];
+    if (cnt >= 8) {
+        if (a.bias) {
+            const f32x4 b0 = reinterpret_cast<const f32x4_u *>(a.bias + n)[0];
+            const f32x4 b1 = reinterpret_cast<const f32x4_u *>(a.bias + n)[1];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        if (i >= cnt)
-            break;
-        float v = acc[i];
-        if (a.bias)
-            v += a.bias[n + i];
-        v = activate(v, a.act);
-        if (a.residual)
-            v += a.io_bf16 ? IoBF16::ld(static_cast<const uint16_t *>(a.residual), at + i)
-                           : static_cast<const float *>(a.residual)[at + i];
-        if (s.bf16)
-            static_cast<uint16_t *>(s.p)[at + i] = bf16_rne(v);
-        else
-            static_cast<float *>(s.p)[at + i] = v;
-    }
-}
-
-// ---- one tile per wave ------------------------------------------------------
-
-// A wave computes RT tiles of 16 rows x 16 columns, its operands loaded
-// straight from memory.
-template <int RT>
-__global__ __launch_bounds__(256) void k_linear_bf16(LinearArgs a, int mtiles) {
-    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-    const int64_t t = (int64_t)blockIdx.x * 4 + wave;
-    const int n0 = (int)(t / mtiles) * 16, m0 = (int)(t % mtiles) * 16 * RT;
-    if (n0 >= a.N)
-        return;
-    const int r = lane & 15, k0 = 8 * (lane >> 4);
-    const uint16_t *w = static_cast<const uint16_t *>(a.w) +
-                        (int64_t)min(n0 + r, a.N - 1) * a.K + k0;
-    const uint16_t *x[RT];
+            for (int i = 0; i < 4; ++i) {
+                v[i] += b0[i];
+                v[i + 4] += b1[i];
+            }
+        }
+        if (a.residual) {
+            if (a.io_bf16) {
+                const u32x4 w = *reinterpret_cast<const u32x4_u *>(
+                    static_cast<const uint16_t *>(a.residual) + at);
 #pragma unroll
-    for (int i = 0; i < RT; ++i)
-        x[i] = static_cast<const uint16_t *>(a.x) +
-               (int64_t)min(m0 + 16 * i + r, a.M - 1) * a.K + k0;
-    f32x4 acc[RT] = {};
-    for (int k = 0; k < a.K; k += 32) {
-        const bool in = k + k0 < a.K;
-        const u32x4 zero = {0, 0, 0, 0};
-        const u32x4 wv = in ? *reinterpret_cast<const u32x4 *>(w + k) : zero;
+                for (int i = 0; i < 4; ++i) {
+                    r[2 * i] = __uint_as_float(w[i] << 16);
+                    r[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
+                }
+            } else {
+                const f32x4_u *p = reinterpret_cast<const f32x4_u *>(
+                    static_cast<const float *>(a.residual) + at);
+                const f32x4 r0 = p[0], r1 = p[1];
 #pragma unroll
-        for (int i = 0; i < RT; ++i) {
-            const u32x4 xv = in ? *reinterpret_cast<const u32x4 *>(x[i] + k) : zero;
-            acc[i] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(
-                __builtin_bit_cast(bf16x8, wv), __builtin_bit_cast(bf16x8, xv), acc[i], 0, 0, 0);
+                for (int i = 0; i < 4; ++i) {
+                    r[i] = r0[i];
+                    r[i + 4] = r1[i];
+                }
+            }
+        }
+    } else {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            if (i < cnt && a.bias)
+                v[i] += a.bias[n + i];
+            if (i < cnt && a.residual)
+                r[i] = a.io_bf16 ? IoBF16::ld(static_cast<const uint16_t *>(a.residual), at + i)
+                                 : static_cast<const float *>(a.residual)[at + i];
         }
     }
+    if (a.act != SSD_ACT_NONE)
 #pragma unroll
-    for (int i = 0; i < RT; ++i)
-        store_tile(a, m0 + 16 * i, n0, acc[i]);
-}
-
-template <int RT>
-__global__ __launch_bounds__(256) void k_linear_f32(LinearArgs a, int mtiles) {
-    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-    const int64_t t = (int64_t)blockIdx.x * 4 + wave;
-    const int n0 = (int)(t / mtiles) * 16, m0 = (int)(t % mtiles) * 16 * RT;
-    if (n0 >= a.N)
+        for (int i = 0; i < 8; ++i)
+            v[i] = activate(v[i], a.act);
+    if (a.residual)
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+            v[i] += r[i];
+    if (cnt >= 8) {
+        if (s.bf16) {
+            u32x4 w;
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                w[i] = bf16_rne(v[2 * i]) | ((uint32_t)bf16_rne(v[2 * i + 1]) << 16);
+            *reinterpret_cast<u32x4_u *>(static_cast<uint16_t *>(s.p) + at) = w;
+        } else {
+            f32x4_u *p = reinterpret_cast<f32x4_u *>(static_cast<float *>(s.p) + at);
+            p[0] = (f32x4){v[0], v[1], v[2], v[3]};
+            p[1] = (f32x4){v[4], v[5], v[6], v[7]};
+        }
         return;
-    const int r = lane & 15, k0 = lane >> 4;   // K is a multiple of 4: no tail
-    const float *w = static_cast<const float *>(a.w) + (int64_t)min(n0 + r, a.N - 1) * a.K + k0;
-    const float *x[RT];
-#pragma unroll
-    for (int i = 0; i < RT; ++i)
-        x[i] = static_cast<const float *>(a.x) +
-               (int64_t)min(m0 + 16 * i + r, a.M - 1) * a.K + k0;
-    f32x4 acc[RT] = {};
-    for (int k = 0; k < a.K; k += 4) {
-        const float wv = w[k];
-#pragma unroll
-        for (int i = 0; i < RT; ++i)
-            acc[i] = __builtin_amdgcn_mfma_f32_16x16x4f32(wv, x[i][k], acc[i], 0, 0, 0);
     }
 #pragma unroll
-    for (int i = 0; i < RT; ++i)
-        store_tile(a, m0 + 16 * i, n0, acc[i]);
+    for (int i = 0; i < 8; ++i)
+        if (i < cnt) {
+            if (s.bf16)
+                static_cast<uint16_t *>(s.p)[at + i] = bf16_rne(v[i]);
+            else
+                static_cast<float *>(s.p)[at + i] = v[i];
+        }
+}
+
+// ---- tiles through LDS --------------------------------------------------------
+
+// The wave's number as a scalar (what is computed from it then is, too).
+__device__ __forceinline__ int wave_id() {
+    return __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+}
+
+typedef __attribute__((address_space(3))) void lds_void;
+
+// A workgroup computes BM rows x BN columns, in (BM / WM) (BN / WN) waves of
+// WM x WN each (16 x 16 tiles). Both operands pass through LDS in tiles of 2 BK
+// bytes of k (BK bf16, BK / 2 fp32), S buffers in turn: the direct loads (global_load_lds, 16 bytes a lane) of the
+// S - 1 tiles ahead run while the matrix cores work on this one. NL waves issue
+// the loads (more than compute, where one tile is all the work of a group).
+// LDS layout: row r of a tile at 2 BK r bytes, its 16-byte piece c at c ^ (r % 8),
+// so that the 16 rows that a fragment read touches spread over the banks. A
+// direct load fills 1 KB in lane order, whole rows or more, so a lane fetches
+// the piece that belongs at its place.
+template <bool F32_, int BM_, int BN_, int WM_, int WN_, int BK_, int S_, int NL_ = 0>
+struct Tile {
+    static constexpr bool F32 = F32_;
+    static constexpr int BM = BM_, BN = BN_, WM = WM_, WN = WN_, BK = BK_, S = S_;
+    static constexpr int NWM = BM / WM, NWN = BN / WN, NW = NWM * NWN;
+    static constexpr int NL = NL_ ? NL_ : NW, WAVES = NL > NW ? NL : NW;
+    static constexpr int FM = WM / 16, FN = WN / 16;
+    static constexpr int PIECES = BK / 8;                 // 16-byte pieces of a row
+    static constexpr int RPL = 64 / PIECES;               // rows of one direct load
+    static constexpr int LX = BM / RPL / NL, LW = BN / RPL / NL;   // loads per wave
+    static constexpr int BYTES = (BM + BN) * BK * 2, XBYTES = BM * BK * 2;
+    static_assert(BM % (RPL * NL) == 0 && BN % (RPL * NL) == 0, "loads divide over the waves");
+    static_assert(S * BYTES <= 160 * 1024, "LDS of a compute unit");
+};
+
+// One direct load of 1 KB: lane l's 16 bytes from base + off to LDS byte
+// lds + 16 l. (An asm statement without register outputs: the compiler, which
+// cannot tell the buffers apart, would wait for all loads in flight before
+// each LDS read; the kernel waits at its barriers instead. m0 is free: the
+// compiler sets it where it needs it.)
+__device__ __forceinline__ void direct_load(uint32_t lds, const char *base, uint32_t off) {
+    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, %2"
+                 :
+                 : "s"(lds), "v"(off), "s"(base)
+                 : "memory");
+}
+
+// Waits for this wave's direct loads except the newest N and its LDS reads,
+// then for the workgroup.
+template <int N>
+__device__ __forceinline__ void loads_barrier() {
+    asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)\n\ts_barrier" : : "n"(N) : "memory");
+}
+
+template <class C>
+struct TileLoader {
+    const char *x, *w;                // the tile's first row
+    uint32_t ox[C::LX], ow[C::LW];    // per-lane byte offsets of the wave's loads
+    uint32_t lx, lw;                  // LDS offsets of the wave's loads in a buffer
+    int nx;                           // loads of x that hold rows below M
+    __device__ __forceinline__ TileLoader(const LinearArgs &a, int m0, int n0) {
+        const int lane = threadIdx.x & 63, wave = wave_id();
+        const uint32_t rb = row_bytes(a);
+        x = static_cast<const char *>(a.x) + (int64_t)m0 * rb;
+        w = static_cast<const char *>(a.w) + (int64_t)n0 * rb;
+        // (rows past the end read the last row; what they give is not stored)
+#pragma unroll
+        for (int i = 0; i < C::LX; ++i)
+            ox[i] = offset(wave * C::LX + i, lane, a.M - 1 - m0, rb);
+#pragma unroll
+        for (int i = 0; i < C::LW; ++i)
+            ow[i] = offset(wave * C::LW + i, lane, a.N - 1 - n0, rb);
+        lx = 1024 * wave * C::LX;
+        lw = C::XBYTES + 1024 * wave * C::LW;
+        nx = (a.M - m0 + C::RPL - 1) / C::RPL - wave * C::LX;
+    }
+    // Byte offset of the lane's piece of load number i of an operand.
+    __device__ static __forceinline__ int piece(int i, int lane) {
+        const int row = i * C::RPL + lane / C::PIECES;
+        return (lane % C::PIECES) ^ (row & 7);
+    }
+    __device__ static __forceinline__ uint32_t offset(int i, int lane, int last, uint32_t rb) {
+        const int row = i * C::RPL + lane / C::PIECES;
+        return (uint32_t)min(row, last) * rb + 16 * piece(i, lane);
+    }
+    __device__ static __forceinline__ uint32_t row_bytes(const LinearArgs &a) {
+        return (uint32_t)a.K * (C::F32 ? 4 : 2);
+    }
+    // Tile at byte kb of the rows, all 2 BK bytes of it there. Loads of x whose rows
+    // are all past M are left out: those rows of the buffer feed columns of the
+    // result that are not stored.
+    __device__ __forceinline__ void load(char *buf, int64_t kb) const {
+        const uint32_t lds = (uint32_t)(uintptr_t)(lds_void *)buf;
+#pragma unroll
+        for (int i = 0; i < C::LX; ++i)
+            if (C::BM > 32 || i < nx)
+                direct_load(lds + lx + 1024 * i, x + kb, ox[i]);
+#pragma unroll
+        for (int i = 0; i < C::LW; ++i)
+            direct_load(lds + lw + 1024 * i, w + kb, ow[i]);
+    }
+    // The last tile when 2 BK does not divide a row: pieces past it are zeros
+    // (left: what is there, in units of 2 bytes).
+    __device__ __forceinline__ void load_tail(char *buf, int64_t kb, int left) const {
+        const int lane = threadIdx.x & 63, wave = wave_id();
+        const u32x4 zero = {0, 0, 0, 0};
+#pragma unroll
+        for (int i = 0; i < C::LX; ++i)
+            *reinterpret_cast<u32x4 *>(buf + lx + 1024 * i + 16 * lane) =
+                8 * piece(wave * C::LX + i, lane) < left
+                    ? *reinterpret_cast<const u32x4 *>(x + kb + ox[i]) : zero;
+#pragma unroll
+        for (int i = 0; i < C::LW; ++i)
+            *reinterpret_cast<u32x4 *>(buf + lw + 1024 * i + 16 * lane) =
+                8 * piece(wave * C::LW + i, lane) < left
+                    ? *reinterpret_cast<const u32x4 *>(w + kb + ow[i]) : zero;
+    }
+};
+
+// One step of a 16 x 16 tile: lane l's operands are 16 bytes of row (column) l % 16
+// at byte 16 (l / 16) of the step.
+template <bool F32>
+__device__ __forceinline__ f32x4 mma_step(const u32x4 &w, const u32x4 &x, f32x4 acc) {
+    if constexpr (F32) {
+        const f32x4 fw = __builtin_bit_cast(f32x4, w), fx = __builtin_bit_cast(f32x4, x);
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            acc = __builtin_amdgcn_mfma_f32_16x16x4f32(fw[i], fx[i], acc, 0, 0, 0);
+        return acc;
+    } else {
+        return __builtin_amdgcn_mfma_f32_16x16x32_bf16(
+            __builtin_bit_cast(bf16x8, w), __builtin_bit_cast(bf16x8, x), acc, 0, 0, 0);
+    }
+}
+
+// NK steps of an LDS tile, from step k0: the w fragments of a step stay,
+// the x fragments come in groups of two, and the reads of the group after next
+// (and of its step's w) go out before this group's MFMAs.
+template <class C, int NK>
+__device__ __forceinline__ void tile_steps(const char *buf, f32x4 (&acc)[C::FM][C::FN],
+                                           int k0 = 0) {
+    constexpr int G = C::FM < 2 ? 1 : 2, NG = C::FM / G;
+    constexpr int AHEAD = 2;   // groups read ahead
+    constexpr int RX = AHEAD + 1, RW = 1 + (AHEAD + NG - 1) / NG;
+    const int lane = threadIdx.x & 63, wave = wave_id();
+    const int r = lane & 15;
+    const char *px = buf + ((wave % C::NWM) * C::WM + r) * (2 * C::BK);
+    const char *pw = buf + C::XBYTES + ((wave / C::NWM) * C::WN + r) * (2 * C::BK);
+    const auto piece = [&](int kk) { return 16 * ((4 * (k0 + kk) + (lane >> 4)) ^ (r & 7)); };
+    u32x4 x[RX][G], w[RW][C::FN];
+    const auto read = [&](int s) {
+        const int kk = s / NG, g = s % NG;
+        if (g == 0)
+#pragma unroll
+            for (int j = 0; j < C::FN; ++j)
+                w[kk % RW][j] = *reinterpret_cast<const u32x4 *>(pw + piece(kk) +
+                                                                  j * 16 * (2 * C::BK));
+#pragma unroll
+        for (int i = 0; i < G; ++i)
+            x[s % RX][i] = *reinterpret_cast<const u32x4 *>(px + piece(kk) +
+                                                             (g * G + i) * 16 * (2 * C::BK));
+    };
+#pragma unroll
+    for (int s = 0; s < AHEAD && s < NK * NG; ++s)
+        read(s);
+#pragma unroll
+    for (int s = 0; s < NK * NG; ++s) {
+        const int kk = s / NG, g = s % NG;
+        if (s + AHEAD < NK * NG)
+            read(s + AHEAD);
+        __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+        for (int i = 0; i < G; ++i)
+#pragma unroll
+            for (int j = 0; j < C::FN; ++j)
+                acc[g * G + i][j] =
+                    mma_step<C::F32>(w[kk % RW][j], x[s % RX][i], acc[g * G + i][j]);
+        __builtin_amdgcn_sched_barrier(0);
+    }
+}
+
+// Which tile a workgroup computes. Workgroup b runs on XCD b % 8, whose L2 the
+// others do not share. Tiles run down the rows, then along the columns. With
+// eight row tiles or more, an XCD that takes every eighth tile sees an eighth of
+// the rows of x. With fewer, it takes a run of tiles instead, all rows of an
+// eighth of the columns, so that w, the larger operand then, goes to one XCD
+// (256 x 2048 x 4096 as 64 x 32 tiles: 15.4 against 20.7 us; 8192 x 8192 x 8192
+// the other way round: 950 against 990 us).
+__device__ __forceinline__ bool tile_of(int b, int mtiles, int ntiles, int &m, int &n) {
+    const int t = mtiles < 8 ? (b & 7) * (int)(gridDim.x >> 3) + (b >> 3) : b;
+    m = t % mtiles;
+    n = t / mtiles;
+    return n < ntiles;
+}
+
+template <class C>
+__global__ __launch_bounds__(64 * C::WAVES) void k_linear_tile(LinearArgs a, int mtiles,
+                                                             int ntiles) {
+    constexpr int S = C::S, BK = C::BK;
+    __shared__ __attribute__((aligned(1024))) char buf[S * C::BYTES];
+    const int wave = wave_id();
+    int m0, n0;
+    if (!tile_of(blockIdx.x, mtiles, ntiles, m0, n0))
+        return;
+    m0 *= C::BM;
+    n0 *= C::BN;
+    const bool loads = C::NL == C::WAVES || wave < C::NL;
+    const bool works = C::NW == C::WAVES || wave < C::NW;
+    const TileLoader<C> ld(a, m0, n0);
+    f32x4 acc[C::FM][C::FN] = {};
+    const int k2 = a.K * (C::F32 ? 2 : 1);   // a row in units of 2 bytes
+    const int full = k2 / BK, left = k2 % BK;
+#pragma unroll
+    for (int t = 0; t < S - 1; ++t)
+        if (t < full && loads)
+            ld.load(buf + t * C::BYTES, t * BK * 2);
+    int slot = 0, ahead = S - 1;      // t % S and (t + S - 1) % S
+    for (int t = 0; t < full; ++t) {
+        // tile t is there when only the loads of the S - 2 tiles after it are in
+        // flight (with loads left out fewer: that waits for more); past the
+        // barrier every wave has read tile t - 1, whose buffer is loaded next
+        if (C::BM > 32 && t + S - 2 < full)
+            loads_barrier<(S - 2) * (C::LX + C::LW)>();
+        else if (t + S - 2 < full)
+            loads_barrier<(S - 2) * C::LW>();
+        else
+            loads_barrier<0>();
+        if (t + S - 1 < full && loads)
+            ld.load(buf + ahead * C::BYTES, (int64_t)(t + S - 1) * BK * 2);
+        if (works)
+            tile_steps<C, BK / 32>(buf + slot * C::BYTES, acc);
+        slot = slot + 1 == S ? 0 : slot + 1;
+        ahead = ahead + 1 == S ? 0 : ahead + 1;
+    }
+    __syncthreads();
+    if (left) {
+        if (loads)
+            ld.load_tail(buf, (int64_t)full * BK * 2, left);
+        __syncthreads();
+        if (works)
+#pragma unroll 1
+            for (int k = 0; k < left; k += 32)
+                tile_steps<C, 1>(buf, acc, k / 32);
+        __syncthreads();
+    }
+    if (!works)
+        return;
+    // Epilogue through LDS, 32 of the wave's rows at a time in its own part of
+    // the buffers, so that lanes store eight columns of a row together. (A row
+    // is WN + 4 floats long: the 16 rows of a tile write to different banks.)
+    constexpr int PITCH = C::WN + 4;
+    constexpr int HALF = C::FM < 2 || 32 * PITCH * 4 * C::NW > S * C::BYTES ? 1 : 2;
+    constexpr int PART = HALF * 16 * PITCH;
+    static_assert(PART * 4 * C::NW <= S * C::BYTES, "fits the buffers");
+    const int lane = threadIdx.x & 63;
+    float *mine = reinterpret_cast<float *>(buf) + wave * PART;
+    const int wm = m0 + (wave % C::NWM) * C::WM, wn = n0 + (wave / C::NWM) * C::WN;
+#pragma unroll
+    for (int h = 0; h < C::FM / HALF; ++h) {
+#pragma unroll
+        for (int i = 0; i < HALF; ++i)
+#pragma unroll
+            for (int j = 0; j < C::FN; ++j)
+                *reinterpret_cast<f32x4 *>(mine + (16 * i + (lane & 15)) * PITCH + 16 * j +
+                                           4 * (lane >> 4)) = acc[h * HALF + i][j];
+        __builtin_amdgcn_wave_barrier();
+#pragma unroll 1
+        for (int e = lane; e < HALF * 16 * (C::WN / 8); e += 64) {
+            const int row = e / (C::WN / 8), col = e % (C::WN / 8) * 8;
+            const int m = wm + h * HALF * 16 + row, n = wn + col;
+            if (m < a.M && n < a.N) {
+                const f32x4 v0 = *reinterpret_cast<const f32x4 *>(mine + row * PITCH + col);
+                const f32x4 v1 = *reinterpret_cast<const f32x4 *>(mine + row * PITCH + col + 4);
+                float v[8] = {v0[0], v0[1], v0[2], v0[3], v1[0], v1[1], v1[2], v1[3]};
+                store_eight(a, m, n, v);
+            }
+        }
+        __builtin_amdgcn_wave_barrier();
+    }
+}
+
+// ---- choice of the tile -----------------------------------------------------
+
+// All shapes give the same bits; the choice is for time alone. A shape's time
+// is modelled as that of its rounds of tiles over the 256 compute units. A
+// round takes fix (us) + K ns, measured at K = 1024 and 4096 with one workgroup
+// on each compute unit (fix1, ns1) and with as many as fit (fix, ns); in
+// between by the line through the two.
+struct Shape {
+    int bm, bn;
+    int fit;                 // workgroups that run on a compute unit at a time
+    float fix1, ns1, fix, ns;
+};
+constexpr int kUnits = 256;
+
+inline float shape_time(const Shape &s, int64_t M, int64_t N, int64_t K) {
+    const int64_t tiles = ((M + s.bm - 1) / s.bm) * ((N + s.bn - 1) / s.bn);
+    const int64_t rounds = tiles / (kUnits * s.fit), rest = tiles - rounds * kUnits * s.fit;
+    const float one = s.fix1 + (float)K * s.ns1 * 1e-3f, full = s.fix + (float)K * s.ns * 1e-3f;
+    float t = (float)rounds * full;
+    if (rest > 0)
+        t += s.fit == 1 ? one
+                        : one + (full - one) * (float)((rest - 1) / kUnits) / (float)(s.fit - 1);
+    return t;
+}
+
+template <int N>
+int best_shape(const Shape (&s)[N], const LinearArgs &a) {
+    int best = 0;
+    float least = shape_time(s[0], a.M, a.N, a.K);
+    for (int i = 1; i < N; ++i) {
+        const float t = shape_time(s[i], a.M, a.N, a.K);
+        if (t < least) {
+            least = t;
+            best = i;
+        }
+    }
+    return best;
+}
+
+template <class C>
+hipError_t launch_tile(const LinearArgs &a, hipStream_t stream) {
+    const int64_t mt = (a.M + C::BM - 1) / C::BM, nt = (a.N + C::BN - 1) / C::BN;
+    // (a multiple of 8: runs of tiles for the XCDs)
+    const dim3 grid((unsigned)((mt * nt + 7) / 8 * 8));
+    k_linear_tile<C><<<grid, dim3(64 * C::WAVES), 0, stream>>>(a, (int)mt, (int)nt);
+    return hipGetLastError();
+}
+
+hipError_t linear_bf16(const LinearArgs &a, hipStream_t stream) {
+    static constexpr Shape kShapes[] = {
+        {16, 16, 3, 0.0f, 1.6f, 0.0f, 3.4f},       {16, 16, 1, 0.5f, 1.0f, 0.5f, 1.0f},
+        {32, 32, 2, 0.5f, 2.3f, 0.5f, 3.0f},       {64, 32, 1, 0.2f, 2.9f, 0.2f, 2.9f},
+        {64, 64, 2, 1.0f, 4.1f, 1.0f, 5.6f},       {128, 64, 2, 1.3f, 5.0f, 2.8f, 7.9f},
+        {128, 128, 2, 4.3f, 8.9f, 5.2f, 10.7f},    {256, 256, 1, 10.0f, 20.6f, 10.0f, 20.6f},
+    };
+    switch (best_shape(kShapes, a)) {
+    case 0: return launch_tile<Tile<false, 16, 16, 16, 16, 256, 3, 4>>(a, stream);
+    case 1: return launch_tile<Tile<false, 16, 16, 16, 16, 512, 5, 8>>(a, stream);
+    case 2: return launch_tile<Tile<false, 32, 32, 16, 16, 128, 4>>(a, stream);
+    case 3: return launch_tile<Tile<false, 64, 32, 32, 16, 256, 3>>(a, stream);
+    case 4: return launch_tile<Tile<false, 64, 64, 32, 32, 64, 4>>(a, stream);
+    case 5: return launch_tile<Tile<false, 128, 64, 32, 32, 64, 3>>(a, stream);
+    case 6: return launch_tile<Tile<false, 128, 128, 32, 64, 64, 2>>(a, stream);
+    default: return launch_tile<Tile<false, 256, 256, 128, 64, 64, 2>>(a, stream);
+    }
+}
+
+// fp32 is bound by the matrix instructions from 32 x 32 on (131 of 157 TFLOP/s
+// peak in full rounds): the shapes differ in how evenly the tiles divide.
+hipError_t linear_f32(const LinearArgs &a, hipStream_t stream) {
+    static constexpr Shape kShapes[] = {
+        {16, 16, 3, 0.0f, 5.8f, 0.4f, 7.4f},       {16, 16, 1, 0.2f, 5.4f, 0.2f, 5.4f},
+        {32, 32, 2, 0.4f, 7.4f, 1.1f, 10.2f},      {64, 32, 3, 0.2f, 11.9f, 2.5f, 23.6f},
+        {64, 64, 2, 1.1f, 19.4f, 3.0f, 30.3f},     {128, 64, 3, 2.4f, 33.3f, 6.8f, 85.1f},
+        {128, 128, 2, 4.8f, 62.5f, 8.4f, 112.0f},  {256, 128, 1, 7.7f, 119.0f, 7.7f, 119.0f},
+    };
+    switch (best_shape(kShapes, a)) {
+    case 0: return launch_tile<Tile<true, 16, 16, 16, 16, 256, 3, 4>>(a, stream);
+    case 1: return launch_tile<Tile<true, 16, 16, 16, 16, 512, 5, 8>>(a, stream);
+    case 2: return launch_tile<Tile<true, 32, 32, 16, 16, 128, 4>>(a, stream);
+    case 3: return launch_tile<Tile<true, 64, 32, 32, 16, 128, 2>>(a, stream);
+    case 4: return launch_tile<Tile<true, 64, 64, 32, 32, 128, 2>>(a, stream);
+    case 5: return launch_tile<Tile<true, 128, 64, 32, 32, 64, 2>>(a, stream);
+    case 6: return launch_tile<Tile<true, 128, 128, 32, 64, 64, 2>>(a, stream);
+    default: return launch_tile<Tile<true, 256, 128, 64, 64, 64, 2>>(a, stream);
+    }
 }
 
 }  // namespace
 
 hipError_t launch_linear(const LinearArgs &a, hipStream_t stream) {
-    const int ntiles = (a.N + 15) / 16;
-    const int rt = a.M > 16 ? 4 : 1;
-    const int mtiles = (a.M + 16 * rt - 1) / (16 * rt);
-    const dim3 grid((unsigned)(((int64_t)ntiles * mtiles + 3) / 4)), block(256);
-    if (a.io_bf16) {
-        if (rt == 1)
-            k_linear_bf16<1><<<grid, block, 0, stream>>>(a, mtiles);
-        else
-            k_linear_bf16<4><<<grid, block, 0, stream>>>(a, mtiles);
-    } else {
-        if (rt == 1)
-            k_linear_f32<1><<<grid, block, 0, stream>>>(a, mtiles);
-        else
-            k_linear_f32<4><<<grid, block, 0, stream>>>(a, mtiles);
-    }
-    return hipGetLastError();
+    return a.io_bf16 ? linear_bf16(a, stream) : linear_f32(a, stream);
 }
 
 }  // namespace ssd

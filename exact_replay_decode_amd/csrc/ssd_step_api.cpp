@@ -27,10 +27,13 @@ int check_linear(int64_t M, int64_t N, int64_t K, int32_t io) {
         return SSD_ERR_DTYPE;
     if (M < 0 || N < 0 || K < 1)
         return SSD_ERR_SHAPE;
-    if (M > kMaxI32 || N > kMaxI32 || K > kMaxI32 - 64 || K % (io == SSD_BF16 ? 8 : 4) != 0)
+    // (a tile's rows lie within 32-bit byte offsets of its first one, and row
+    // numbers up to a tile past the end are whole numbers of 32 bits)
+    if (M > kMaxI32 - 65536 || N > kMaxI32 - 65536 || K > (1 << 20) ||
+        K % (io == SSD_BF16 ? 8 : 4) != 0)
         return SSD_ERR_UNSUPPORTED;
     // 16 x 16 tiles, the smallest unit of a launch, within one grid dimension
-    if (((M + 15) / 16) * ((N + 15) / 16) > kMaxI32)
+    if (((M + 15) / 16) * ((N + 15) / 16) > kMaxI32 - 8)
         return SSD_ERR_UNSUPPORTED;
     return SSD_OK;
 }

@@ -38,11 +38,11 @@ typedef enum {
  *   residual  [M,N] io_dtype, or NULL
  *   out       [M,N] out_dtype (SSD_F32 or SSD_BF16); may be `residual`
  *             itself when the dtypes agree, and aliases nothing else
- * The sum is one fp32 chain over k ascending (matrix-core steps of 32 k in
- * bf16, of 4 in fp32; a bf16 product is exact in fp32), the epilogue is
+ * The sum is one fp32 chain over k in a fixed order (matrix-core steps of 32
+ * k in bf16, of 4 in fp32; a bf16 product is exact in fp32), the epilogue is
  * fp32, and the result is rounded once. The bits of a row do not depend on M.
- * M >= 0, N >= 0, K >= 1; K a multiple of 8 (bf16) or 4 (fp32), else
- * SSD_ERR_UNSUPPORTED; x and w 16-byte aligned (the others need their natural
+ * M >= 0, N >= 0, K >= 1; K a multiple of 8 (bf16) or 4 (fp32) and at most
+ * 1048576, else SSD_ERR_UNSUPPORTED; x and w 16-byte aligned (the others need their natural
  * alignment). */
 int ssd_linear(int64_t M, int64_t N, int64_t K, int32_t io_dtype,
                int32_t out_dtype, int32_t activation, const void *x,

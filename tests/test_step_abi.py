@@ -53,7 +53,7 @@ def linear(M=4, N=8, K=16, io=BF16, out=BF16, act=0, x=A, w=A, bias=None, res=No
     (dict(M=-1), SHAPE), (dict(N=-1), SHAPE), (dict(K=0), SHAPE), (dict(K=-8), SHAPE),
     (dict(K=12), UNSUP), (dict(io=F32, out=F32, K=6), UNSUP), (dict(K=4), UNSUP),
     (dict(M=2 ** 31), UNSUP), (dict(N=2 ** 31), UNSUP), (dict(M=2 ** 30, N=2 ** 30), UNSUP),
-    (dict(K=2 ** 31 - 8), UNSUP), (dict(io=2), DTYPE), (dict(out=-1), DTYPE),
+    (dict(K=2 ** 20 + 8), UNSUP), (dict(io=2), DTYPE), (dict(out=-1), DTYPE),
     (dict(act=4), UNSUP), (dict(act=-1), UNSUP), (dict(x=None), NULL), (dict(w=None), NULL),
     (dict(o=None), NULL), (dict(x=A + 8), ALIGN), (dict(w=A + 2), ALIGN),
     (dict(bias=A + 2), ALIGN), (dict(res=A + 1), ALIGN), (dict(o=A + 1), ALIGN),
