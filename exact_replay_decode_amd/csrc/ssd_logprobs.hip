@@ -11,17 +11,17 @@
 // depend neither on the number of rows nor on how many waves share the row
 // (4, or 16 when there are few rows).
 //
-// The best top_k in four short steps after the pass, from what the softmax
-// needs anyway, the maxima of each lane's 32 elements of a chunk (a segment;
-// kept in LDS): the top_k-th largest lane maximum of a wave bounds the row's
-// top_k-th best from below, the best of these bounds leaves few lanes, their
-// exact top_k-th largest leaves few more than top_k segments, and only those
-// are read again, a wave two segments at a time. The candidates' places are
-// counted. Keys (value, then lower index) are unique 64-bit numbers, so the
-// result does not depend on the order of any of this. Masked elements are no
-// candidates: when fewer than top_k are left, the lowest masked indices follow.
-// A row with too many equal best values for the lists is read again element
-// by element into sorted lists, one per wave, which are then joined.
+// The best top_k in short steps after the pass, from what the softmax needs
+// anyway, the maxima of each lane's 32 elements of a chunk (a segment; kept in
+// LDS): the lanes form 128 groups (64 for a small top_k), the top_k-th largest of the groups' maxima
+// bounds the row's top_k-th best from below, and only the segments that reach
+// it are read again (for top_k = 20 about 25), a wave two at a time. The
+// candidates' places are counted. Keys (value, then lower index) are unique
+// 64-bit numbers, so the result does not depend on the order of any of this.
+// Masked elements are no candidates: when fewer than top_k are left, the lowest
+// masked indices follow. A row with too many best values for the lists (equal
+// ones) is read again element by element into sorted lists, one per wave, which
+// are then joined.
 // rank counts the elements ahead of the token with one comparison each.
 //
 // Measured: 4096 rows of 50280 bf16 in 89 us without alternatives (4.6 TB/s), where
@@ -38,8 +38,8 @@ namespace {
 constexpr int kStreams = 16;
 constexpr int kPerLane = 32;
 constexpr int kChunkElems = 64 * kPerLane;
-constexpr int kSegs = 1024;       // segments read again, and lane maxima compared
-constexpr int kCands = 512;       // candidates
+constexpr int kSegs = 1024;       // segments read again
+constexpr int kCands = 1024;      // candidates (top_k = 64: 90 in the mean)
 
 // A wave's chunk: 32 elements per lane in 16-byte pieces, piece v of lane l at
 // element (64 v + l) E. Rows start anywhere (V may be odd), so the loads are
@@ -174,20 +174,6 @@ struct TopList {
     }
 };
 
-// The k-th largest of the lanes' values (no NaN among them), 1 <= k <= 64.
-__device__ __forceinline__ float wave_kth(float v, int k) {
-    const int lane = threadIdx.x & 63;
-    int rank = 0;
-#pragma unroll
-    for (int i = 0; i < 64; ++i) {
-        const float o = __int_as_float(__builtin_amdgcn_readlane(__float_as_int(v), i));
-        rank += o > v || (o == v && i < lane);
-    }
-    const uint64_t at = __ballot(rank == k - 1);
-    return __int_as_float(__builtin_amdgcn_readlane(
-        __float_as_int(v), (int)__ffsll((unsigned long long)at) - 1));
-}
-
 // Place of a lane's entry in a list that *count numbers: one LDS atomic a wave.
 __device__ __forceinline__ int append_at(uint64_t m, int *count) {
     int base = 0;
@@ -215,6 +201,29 @@ __device__ __forceinline__ float wave_max(float v) {
     v = fmaxf(v, dpp_or_own<0x142, 0xa>(v));
     v = fmaxf(v, dpp_or_own<0x143, 0xc>(v));
     return lane63(v);
+}
+
+// The k-th largest of the lanes' values (no NaN among them), 1 <= k <= 64: the
+// least value with fewer than k above it; of 64 values, and of 128.
+__device__ __forceinline__ float wave_kth(float v, int k) {
+    int above = 0;
+#pragma unroll
+    for (int i = 0; i < 64; ++i)
+        above += __int_as_float(__builtin_amdgcn_readlane(__float_as_int(v), i)) > v;
+    return -wave_max(above < k ? -v : -INFINITY);
+}
+__device__ __forceinline__ float wave_kth(float v, float w, int k) {
+    int av = 0, aw = 0;
+#pragma unroll
+    for (int i = 0; i < 64; ++i) {
+        const float a = __int_as_float(__builtin_amdgcn_readlane(__float_as_int(v), i));
+        const float b = __int_as_float(__builtin_amdgcn_readlane(__float_as_int(w), i));
+        av += a > v;
+        aw += a > w;
+        av += b > v;
+        aw += b > w;
+    }
+    return -wave_max(fmaxf(av < k ? -v : -INFINITY, aw < k ? -w : -INFINITY));
 }
 
 // e^d by one v_exp_f32
@@ -245,16 +254,18 @@ __global__ __launch_bounds__(64 * NW) void k_logprobs(LogprobArgs a) {
     using T = typename IO::T;
     constexpr int E = Chunk<IO>::E, NV = Regs<IO>::NV, ORD = Segs<NW>::ORD;
     constexpr int LIST = NW == 4 ? 256 : 128;
-    __shared__ float smax[TOP ? NW * ORD * 64 : 1];
-    __shared__ uint32_t few[TOP ? kSegs : 1];       // lane maxima, then segments
-    __shared__ uint64_t cand[TOP ? kCands : 1];
+    // segment maxima; past the listing of the segments the candidates, or the lists
+    __shared__ __attribute__((aligned(8))) float smax[TOP ? NW * ORD * 64 : 1];
+    __shared__ uint32_t few[TOP ? kSegs : 1];       // segments
+    uint64_t *cand = reinterpret_cast<uint64_t *>(smax);
     __shared__ float st[kStreams][3];
     __shared__ int ahead_of[NW], ln[NW];
-    __shared__ float tw[NW];
+    __shared__ float gm[128];
     __shared__ float fin[3];
-    __shared__ int count[3];
+    __shared__ int count[2];
     __shared__ float tau_row;
     static_assert(sizeof(uint64_t) * NW * LIST <= sizeof(float) * NW * ORD * 64, "in smax's place");
+    static_assert(sizeof(uint64_t) * kCands <= sizeof(float) * NW * ORD * 64, "in smax's place");
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int64_t t = blockIdx.x;
     const int V = a.V;
@@ -272,7 +283,7 @@ __global__ __launch_bounds__(64 * NW) void k_logprobs(LogprobArgs a) {
     // chunks of a wave per row of its segment maxima
     const int wchunks = (kStreams / NW) * ((nchunks + kStreams - 1) / kStreams);
     const int R = (wchunks + ORD - 1) / ORD;
-    if (TOP && threadIdx.x < 3)
+    if (TOP && threadIdx.x < 2)
         count[threadIdx.x] = 0;
 
     int ahead = 0, ord = 0;
@@ -350,24 +361,36 @@ __global__ __launch_bounds__(64 * NW) void k_logprobs(LogprobArgs a) {
     if (lane == 0)
         ahead_of[wave] = ahead;
     if constexpr (TOP) {
-        const float tau = wave_kth(best, a.k);
-        if (lane == 0)
-            tw[wave] = tau;
+        // maxima of groups of NW / 2 lanes, in the group's last lane (DPP row
+        // shifts reach the lanes below within 16)
+        static_assert(NW == 4 || NW == 16, "128 groups");
+        float g = fmaxf(best, dpp_or_own<0x111, 0xf>(best));
+        if constexpr (NW == 16) {
+            g = fmaxf(g, dpp_or_own<0x112, 0xf>(g));
+            g = fmaxf(g, dpp_or_own<0x114, 0xf>(g));
+        }
+        if (lane % (NW / 2) == NW / 2 - 1)
+            gm[(wave * 64 + lane) / (NW / 2)] = g;
     }
     __syncthreads();
 
+    if (TOP && wave == 1) {
+        // (64 groups bound a small top_k well enough; the other waves wait here:
+        // 94 against 98 us for 4096 x 50280, top 5)
+        const float g = gm[2 * lane], h = gm[2 * lane + 1];
+        const float tau = a.k <= 24 ? wave_kth(fmaxf(g, h), a.k) : wave_kth(g, h, a.k);
+        if (lane == 0)
+            tau_row = tau;
+    }
     if (wave == 0) {
+        // the streams' sums joined, a lane each
         Stat z = {-INFINITY, 0.0f, 0.0f};
-        for (int i = 0; i < kStreams; ++i) {
-            Stat o = {st[i][0], st[i][1], st[i][2]};
-            const float m = fmaxf(z.m, o.m);
-            if (m > z.m)
-                z.raise(m);
-            if (m > o.m)
-                o.raise(m);
-            z.s += o.s;
-            z.u += o.u;
-        }
+        if (lane < kStreams)
+            z = {st[lane][0], st[lane][1], st[lane][2]};
+        const float m = wave_max(z.m);
+        if (m > z.m)
+            z.raise(m);
+        z = {m, lane63(wave_scan_inclusive(z.s)), lane63(wave_scan_inclusive(z.u))};
         const bool none = z.m == -INFINITY && z.s == 0.0f;   // nothing left, and no NaN
         const bool bad = !(z.s < INFINITY);                    // a NaN or +inf in the row
         const float ls = none ? 0.0f : logf(z.s);
@@ -400,19 +423,6 @@ __global__ __launch_bounds__(64 * NW) void k_logprobs(LogprobArgs a) {
     if constexpr (!TOP)
         return;
 
-    // the best of the waves' bounds, and the lanes that reach it
-    float tau = tw[0];
-#pragma unroll
-    for (int w = 1; w < NW; ++w)
-        tau = fmaxf(tau, tw[w]);
-    {
-        const uint64_t m = __ballot(best >= tau && best > -INFINITY);
-        if (m) {
-            const int at = append_at(m, &count[0]);
-            if (((m >> lane) & 1) && at < kSegs)
-                few[at] = __float_as_uint(best);
-        }
-    }
     __syncthreads();
     int32_t *ids = a.top_ids + t * a.k;
     float *lps = a.top_logprobs + t * a.k;
@@ -423,36 +433,20 @@ __global__ __launch_bounds__(64 * NW) void k_logprobs(LogprobArgs a) {
         }
         return;
     }
-    // their top_k-th largest (there are top_k of them unless the bound is -inf)
-    const int n1 = count[0];
-    if (n1 <= kSegs && n1 >= a.k)
-        for (int i = threadIdx.x; i < n1; i += 64 * NW) {
-            const float v = __uint_as_float(few[i]);
-            int rank = 0;
-#pragma unroll 8
-            for (int j = 0; j < n1; ++j) {
-                const float o = __uint_as_float(few[j]);
-                rank += o > v || (o == v && j < i);
-            }
-            if (rank == a.k - 1)
-                tau_row = v;
-        }
-    __syncthreads();
-    if (n1 <= kSegs && n1 >= a.k)
-        tau = tau_row;
-    // the segments that reach it (few is free: everyone has read tau_row)
+    // the segments that reach the bound
+    const float tau = tau_row;
     const int ords = (ord + R - 1) / R;
     for (int o = 0; o < ords; ++o) {
         const float s = smax[(wave * ORD + o) * 64 + lane];
         const uint64_t m = __ballot(s >= tau && s > -INFINITY);
         if (m) {
-            const int at = append_at(m, &count[1]);
+            const int at = append_at(m, &count[0]);
             if (((m >> lane) & 1) && at < kSegs)
                 few[at] = (uint32_t)((wave * ORD + o) * 64 + lane);
         }
     }
     __syncthreads();
-    const int nsegs = count[1];
+    const int nsegs = count[0];
     if (nsegs <= kSegs) {
         // a wave reads two segments at a time: lane l element l % 32 of one
         for (int p = 2 * wave; p < nsegs; p += 2 * NW) {
@@ -477,7 +471,7 @@ __global__ __launch_bounds__(64 * NW) void k_logprobs(LogprobArgs a) {
                 const float x = in ? IO::ld(row, i) : -INFINITY;
                 const uint64_t m = __ballot(x >= tau && x > -INFINITY);
                 if (m) {
-                    const int to = append_at(m, &count[2]);
+                    const int to = append_at(m, &count[1]);
                     if (((m >> lane) & 1) && to < kCands)
                         cand[to] = key_of(x, (int)i);
                 }
@@ -485,7 +479,7 @@ __global__ __launch_bounds__(64 * NW) void k_logprobs(LogprobArgs a) {
         }
     }
     __syncthreads();
-    const int n = count[2];
+    const int n = count[1];
     if (nsegs <= kSegs && n <= kCands) {
         for (int i = threadIdx.x; i < n; i += 64 * NW) {
             const uint64_t me = cand[i];

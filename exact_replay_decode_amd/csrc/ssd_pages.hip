@@ -32,25 +32,39 @@ typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
 
 // ---- copying ----------------------------------------------------------------
 
-// n16 16-byte pieces, by the whole workgroup.
-__device__ __forceinline__ void copy16(void *dst, const void *src, int64_t n16) {
+// n16 16-byte pieces, by the whole workgroup: eight loads in flight per thread
+// before the first store. go() is asked between the first loads and the first
+// store, so that what it waits for and the data are under way together; without
+// it nothing is stored.
+template <class Go>
+__device__ __forceinline__ void copy16(void *dst, const void *src, int64_t n16, Go go) {
     constexpr int B = 8;
     u32x4 *d = static_cast<u32x4 *>(dst);
     const u32x4 *s = static_cast<const u32x4 *>(src);
-    for (int64_t e0 = threadIdx.x; e0 < n16; e0 += B * kCopy) {
+    bool asked = false;
+    for (int64_t base = 0; base < n16; base += B * kCopy) {
+        const int64_t e0 = base + threadIdx.x;
         u32x4 v[B];
 #pragma unroll
         for (int i = 0; i < B; ++i) {
             const int64_t e = e0 + i * kCopy;
             v[i] = s[e < n16 ? e : n16 - 1];
         }
+        if (!asked) {
+            if (!go())
+                return;
+            asked = true;
+        }
 #pragma unroll
         for (int i = 0; i < B; ++i) {
             const int64_t e = e0 + i * kCopy;
             if (e < n16)
-                d[e] = v[i];
+                __builtin_nontemporal_store(v[i], d + e);
         }
     }
+}
+__device__ __forceinline__ void copy16(void *dst, const void *src, int64_t n16) {
+    copy16(dst, src, n16, [] { return true; });
 }
 
 // n 2-byte elements (raw dt rows, whose arrays have natural alignment only).
@@ -92,18 +106,16 @@ __global__ __launch_bounds__(kCopy) void k_cache_copy(CopyArgs a, int ns, int nb
     int part = blockIdx.y;
     const int d = a.dst_idx[b], s = a.src_idx[b];
     const bool in = d >= 0 && d < a.dst.num_slots && s >= 0 && s < a.src.num_slots;
-    const int len = in ? a.src.buf_len[s] : -1;
     const bool same = in && a.dst.state == a.src.state && d == s;
-    const bool ok = in && len >= 0 && len < a.src.Q && !same && rows_ok(a.src, s, len) &&
-                    rows_ok(a.dst, d, len);
-    if (part == 0 && threadIdx.x == 0 && a.copied)
-        a.copied[b] = ok || same;
-    if (!ok)
+    if (!in || same) {
+        if (part == 0 && threadIdx.x == 0 && a.copied)
+            a.copied[b] = same;
         return;
-    if (part == 0 && threadIdx.x == 0) {
-        a.dst.buf_len[d] = len;
-        a.dst.boundary_pos[d] = a.src.boundary_pos[s];
     }
+    const int len = a.src.buf_len[s];
+    const auto ok = [&] {
+        return len >= 0 && len < a.src.Q && rows_ok(a.src, s, len) && rows_ok(a.dst, d, len);
+    };
     if (part < ns + nb) {
         // [0, ns): fp32 state, [ns, ns + nb): the bf16 copy
         const bool bf = part >= ns;
@@ -114,9 +126,22 @@ __global__ __launch_bounds__(kCopy) void k_cache_copy(CopyArgs a, int ns, int nb
         char *dst = bf ? static_cast<char *>(a.dst.state_bf)
                        : reinterpret_cast<char *>(a.dst.state);
         const int64_t n = size - at < kPiece ? size - at : kPiece;
-        copy16(dst + d * size + at, src + s * size + at, n / 16);
+        copy16(dst + d * size + at, src + s * size + at, n / 16, [&] {
+            const bool go = ok();
+            if (part == 0 && threadIdx.x == 0) {
+                if (a.copied)
+                    a.copied[b] = go;
+                if (go) {
+                    a.dst.buf_len[d] = len;
+                    a.dst.boundary_pos[d] = a.src.boundary_pos[s];
+                }
+            }
+            return go;
+        });
         return;
     }
+    if (!ok())
+        return;
     part -= ns + nb;
     const int pos = part * kRowGroup;
     if (pos >= len)
@@ -161,8 +186,8 @@ __global__ __launch_bounds__(kCopy) void k_cache_free(SlotMap c, RowBytes r, int
 }
 
 __global__ __launch_bounds__(256) void k_pages_trim(SlotMap c, int n, const int32_t *slot_idx) {
-    const int64_t i = (int64_t)blockIdx.x * blockDim.x + threadIdx.x;
-    const int b = (int)(i / c.npp), e = (int)(i % c.npp);
+    const uint32_t i = blockIdx.x * blockDim.x + threadIdx.x;   // n npp < 2^31
+    const int b = (int)(i / (uint32_t)c.npp), e = (int)(i % (uint32_t)c.npp);
     if (b >= n)
         return;
     const int s = slot_idx ? slot_idx[b] : b;
@@ -200,6 +225,37 @@ __device__ __forceinline__ int block_exclusive(int v, int *red, int *total) {
     return before + x - v;
 }
 
+// Place of the r-th set bit of the words word(0), word(1), .., of which thread t
+// owns the `per` words from t per on and before[t] bits lie below: a search for
+// the owner, a walk over its words, a binary search in the word.
+template <class Word>
+__device__ __forceinline__ int nth_bit(const int32_t *before, int r, int per, Word word) {
+    int lo = 0, hi = kPlan - 1;   // last thread whose before[] is <= r
+    while (lo < hi) {
+        const int mid = (lo + hi + 1) >> 1;
+        if (before[mid] <= r)
+            lo = mid;
+        else
+            hi = mid - 1;
+    }
+    r -= before[lo];
+    int w = lo * per;
+    uint32_t f = word(w);
+    for (int k; r >= (k = __popc(f)); f = word(++w))
+        r -= k;
+    int at = 0;
+#pragma unroll
+    for (int s = 16; s > 0; s >>= 1) {
+        const int k = __popc(f & ((1u << s) - 1u));
+        if (r >= k) {
+            r -= k;
+            f >>= s;
+            at += s;
+        }
+    }
+    return w * 32 + at;
+}
+
 // The used pages as a bitmap in LDS, and the free ones by rank.
 struct PageBits {
     uint32_t *bits;       // [words], a set bit is a used page
@@ -218,11 +274,18 @@ struct PageBits {
         for (int w = threadIdx.x; w < words; w += kPlan)
             bits[w] = 0;
         __syncthreads();
-        const int n = c.num_slots * c.npp;
-        for (int i = threadIdx.x; i < n; i += kPlan) {
-            const int p = c.pages[i];
-            if (page_ok(c, p))
-                atomicOr(&bits[p >> 5], 1u << (p & 31));
+        // (eight entries a thread in flight: the table's latency, not its size,
+        // is what this costs)
+        const int64_t n = (int64_t)c.num_slots * c.npp;
+        for (int64_t i0 = threadIdx.x; i0 < n; i0 += 8 * kPlan) {
+            int p[8];
+#pragma unroll
+            for (int k = 0; k < 8; ++k)
+                p[k] = i0 + k * kPlan < n ? c.pages[i0 + k * kPlan] : -1;
+#pragma unroll
+            for (int k = 0; k < 8; ++k)
+                if (page_ok(c, p[k]))
+                    atomicOr(&bits[p[k] >> 5], 1u << (p[k] & 31));
         }
         __syncthreads();
         const int w0 = threadIdx.x * per, w1 = min(w0 + per, words);
@@ -233,27 +296,39 @@ struct PageBits {
         __syncthreads();
     }
     // the r-th free page, 0 <= r < nfree
-    __device__ int free_page(int r) const {
-        int lo = 0, hi = kPlan - 1;   // last thread whose first[] is <= r
-        while (lo < hi) {
-            const int mid = (lo + hi + 1) >> 1;
-            if (first[mid] <= r)
-                lo = mid;
-            else
-                hi = mid - 1;
-        }
-        r -= first[lo];
-        for (int w = lo * per;; ++w) {
-            uint32_t f = ~bits[w] & valid(w);
-            const int k = __popc(f);
-            if (r >= k) {
-                r -= k;
-                continue;
-            }
-            while (r-- > 0)
-                f &= f - 1;
-            return w * 32 + __ffs(f) - 1;
-        }
+    __device__ __forceinline__ int free_page(int r) const {
+        return nth_bit(first, r, per, [&](int w) { return ~bits[w] & valid(w); });
+    }
+};
+
+// A request: its slot (-1: skipped), the pages its tokens span and the ones it
+// lacks, as a bit mask (a slot has at most kMaxQ / 16 = 16 pages).
+struct Request {
+    int slot, lack;
+    __device__ __forceinline__ Request(const ReserveArgs &a, int b) : slot(-1), lack(0) {
+        const SlotMap &c = a.c;
+        if (b >= a.n)
+            return;
+        const int s = a.slot_idx ? a.slot_idx[b] : b;
+        const int like = a.like_idx ? a.like_idx[b] : s;
+        if (s < 0 || s >= c.num_slots || like < 0 || like >= c.num_slots)
+            return;
+        const int32_t *row = c.pages + (int64_t)s * c.npp;
+        int e[kMaxQ / 16];
+#pragma unroll
+        for (int i = 0; i < kMaxQ / 16; ++i)
+            e[i] = i < c.npp ? row[i] : 0;
+        const int len = c.buf_len[like];
+        int tok = a.tokens ? a.tokens[b] : a.tokens_all;
+        tok = tok < 0 ? 0 : (tok > c.Q ? c.Q : tok);
+        if (len < 0 || len >= c.Q)
+            return;
+        slot = s;
+        const int pages = (min(len + tok, c.Q) + (1 << c.shift) - 1) >> c.shift;
+#pragma unroll
+        for (int i = 0; i < kMaxQ / 16; ++i)
+            if (i < pages && !page_ok(c, e[i]))
+                lack |= 1 << i;
     }
 };
 
@@ -262,37 +337,24 @@ __global__ __launch_bounds__(kPlan) void k_pages_reserve(ReserveArgs a) {
     __shared__ int32_t first[kPlan];
     __shared__ int red[kPlan / 64];
     const SlotMap c = a.c;
+    // (the first requests' loads run beside the table's)
+    Request q(a, threadIdx.x);
     const PageBits pb(c, bits, first, red);
     int asked = 0;   // pages asked for by the entries before this batch
     for (int b0 = 0; b0 < a.n; b0 += kPlan) {
         const int b = b0 + threadIdx.x;
-        int slot = -1, npages = 0, need = 0;
-        if (b < a.n) {
-            slot = a.slot_idx ? a.slot_idx[b] : b;
-            const int like = a.like_idx ? a.like_idx[b] : slot;
-            if (slot < 0 || slot >= c.num_slots || like < 0 || like >= c.num_slots) {
-                slot = -1;
-            } else {
-                const int len = c.buf_len[like];
-                int tok = a.tokens ? a.tokens[b] : a.tokens_all;
-                tok = tok < 0 ? 0 : (tok > c.Q ? c.Q : tok);
-                if (len < 0 || len >= c.Q)
-                    slot = -1;
-                else
-                    npages = (min(len + tok, c.Q) + (1 << c.shift) - 1) >> c.shift;
-            }
-        }
-        int32_t *row = c.pages + (int64_t)(slot < 0 ? 0 : slot) * c.npp;
-        for (int i = 0; i < npages; ++i)
-            need += !page_ok(c, row[i]);
+        if (b0 > 0)
+            q = Request(a, b);
+        const int need = __popc(q.lack);
         int total;
         int r = asked + block_exclusive(need, red, &total);
         asked += total;
-        const bool served = slot >= 0 && (need == 0 || r + need <= pb.nfree);
-        if (served && need > 0)
-            for (int i = 0; i < npages; ++i)
-                if (!page_ok(c, row[i]))
-                    row[i] = pb.free_page(r++);
+        const bool served = q.slot >= 0 && (need == 0 || r + need <= pb.nfree);
+        if (served) {
+            int32_t *row = c.pages + (int64_t)q.slot * c.npp;
+            for (int m = q.lack; m; m &= m - 1)
+                row[__ffs(m) - 1] = pb.free_page(r++);
+        }
         if (b < a.n && a.granted)
             a.granted[b] = served;
     }
@@ -313,29 +375,35 @@ __global__ __launch_bounds__(kPlan) void k_compact_plan(SlotMap c, int32_t *used
     int mine = 0, moves;
     for (int w = w0; w < w1; ++w)
         mine += __popc(movers(w));
-    int j = block_exclusive(mine, red, &moves);
-    high[threadIdx.x] = j;
+    high[threadIdx.x] = block_exclusive(mine, red, &moves);
     if (threadIdx.x == 0) {
         used[0] = U;
         work[0] = moves;
     }
-    for (int w = w0; w < w1; ++w)
-        for (uint32_t m = movers(w); m; m &= m - 1, ++j) {
-            work[2 + 2 * j] = w * 32 + __ffs(m) - 1;
-            work[3 + 2 * j] = pb.free_page(j);
-        }
     __syncthreads();
-    const int n = c.num_slots * c.npp;
-    for (int i = threadIdx.x; i < n; i += kPlan) {
-        const int p = c.pages[i];
-        if (!page_ok(c, p) || p < U)
-            continue;
-        const int w = p >> 5, t = w / pb.per;
-        int rank = high[t];
-        for (int v = t * pb.per; v < w; ++v)
-            rank += __popc(movers(v));
-        rank += __popc(movers(w) & ((1u << (p & 31)) - 1u));
-        c.pages[i] = pb.free_page(rank);
+    // the j-th mover goes to the j-th free page; a thread each
+    for (int j = threadIdx.x; j < moves; j += kPlan) {
+        work[2 + 2 * j] = nth_bit(high, j, pb.per, movers);
+        work[3 + 2 * j] = pb.free_page(j);
+    }
+    const int64_t n = (int64_t)c.num_slots * c.npp;
+    for (int64_t i0 = threadIdx.x; i0 < n; i0 += 8 * kPlan) {
+        int e[8];
+#pragma unroll
+        for (int k = 0; k < 8; ++k)
+            e[k] = i0 + k * kPlan < n ? c.pages[i0 + k * kPlan] : -1;
+#pragma unroll
+        for (int k = 0; k < 8; ++k) {
+            const int p = e[k];
+            if (!page_ok(c, p) || p < U)
+                continue;
+            const int w = p >> 5, t = w / pb.per;
+            int rank = high[t];
+            for (int v = t * pb.per; v < w; ++v)
+                rank += __popc(movers(v));
+            rank += __popc(movers(w) & ((1u << (p & 31)) - 1u));
+            c.pages[i0 + k * kPlan] = pb.free_page(rank);
+        }
     }
 }
 

@@ -197,11 +197,12 @@ def ssd_token_logprobs(logits, tokens, top_k=0, out: TokenLogprobs | None = None
     _chk(tokens, "tokens", (T,), torch.int32, dev)
     k = int(top_k)
     if out is None:
-        f = torch.empty((2, T), dtype=torch.float32, device=dev)
+        f, i = torch.float32, torch.int32
         out = TokenLogprobs(
-            f[0], f[1], torch.empty((T,), dtype=torch.int32, device=dev),
-            torch.empty((T, k), dtype=torch.int32, device=dev) if k > 0 else None,
-            torch.empty((T, k), dtype=torch.float32, device=dev) if k > 0 else None)
+            torch.empty((T,), dtype=f, device=dev), torch.empty((T,), dtype=f, device=dev),
+            torch.empty((T,), dtype=i, device=dev),
+            torch.empty((T, k), dtype=i, device=dev) if k > 0 else None,
+            torch.empty((T, k), dtype=f, device=dev) if k > 0 else None)
     else:
         _chk(out.logprob, "logprob", (T,), torch.float32, dev)
         if out.entropy is not None:
