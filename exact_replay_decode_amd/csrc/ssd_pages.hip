@@ -102,8 +102,12 @@ __device__ __forceinline__ bool rows_ok(const SlotMap &c, int slot, int n) {
 // bf16 copy, the rest 16 buffered rows each. The list runs along x, so that
 // the copies of one source (a fork) read it at the same time.
 __global__ __launch_bounds__(kCopy) void k_cache_copy(CopyArgs a, int ns, int nb) {
-    const int b = blockIdx.x;
+    // every XCD takes a run of entries: the copies of one source read it
+    // through one L2
+    const int b = (int)(blockIdx.x & 7) * (int)(gridDim.x >> 3) + (int)(blockIdx.x >> 3);
     int part = blockIdx.y;
+    if (b >= a.n)
+        return;
     const int d = a.dst_idx[b], s = a.src_idx[b];
     const bool in = d >= 0 && d < a.dst.num_slots && s >= 0 && s < a.src.num_slots;
     const bool same = in && a.dst.state == a.src.state && d == s;
@@ -470,7 +474,7 @@ hipError_t launch_cache_free(const SlotMap &c, const RowBytes &r, int32_t n,
 hipError_t launch_cache_copy(const CopyArgs &a, hipStream_t stream) {
     const int ns = pieces(a.r.state), nb = pieces(a.r.state / 2);
     const int parts = ns + nb + a.src.Q / kRowGroup;
-    k_cache_copy<<<dim3(a.n, parts), dim3(kCopy), 0, stream>>>(a, ns, nb);
+    k_cache_copy<<<dim3((a.n + 7u) / 8u * 8u, parts), dim3(kCopy), 0, stream>>>(a, ns, nb);
     return hipGetLastError();
 }
 
