@@ -65,7 +65,7 @@ __device__ __forceinline__ void store_eight(const LinearArgs &a, int m, int n, f
     if (a.nseg > 1 && n >= s.n1)
         s = n >= a.seg[1].n1 ? a.seg[2] : a.seg[1];
     const int64_t at = (int64_t)m * (s.n1 - s.n0) + (n - s.n0);
-    const int cnt = a.N - n;
+    const int cnt = a.hi - n;
     float r[8];
     if (cnt >= 8) {
         if (a.bias) {
@@ -191,6 +191,13 @@ __device__ __forceinline__ void loads_barrier() {
     asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)\n\ts_barrier" : : "n"(N) : "memory");
 }
 
+// What a row's pieces are exchanged by: eight rows that are read together
+// cover the 128 bytes of a bank row (rows of 64 bytes: in pairs).
+template <class C>
+__device__ __forceinline__ int swizzle(int row) {
+    return C::PIECES >= 8 ? row & 7 : (row >> 1) & 3;
+}
+
 template <class C>
 struct TileLoader {
     const char *x, *w;                // the tile's first row
@@ -208,7 +215,7 @@ struct TileLoader {
             ox[i] = offset(wave * C::LX + i, lane, a.M - 1 - m0, rb);
 #pragma unroll
         for (int i = 0; i < C::LW; ++i)
-            ow[i] = offset(wave * C::LW + i, lane, a.N - 1 - n0, rb);
+            ow[i] = offset(wave * C::LW + i, lane, a.hi - 1 - n0, rb);
         lx = 1024 * wave * C::LX;
         lw = C::XBYTES + 1024 * wave * C::LW;
         nx = (a.M - m0 + C::RPL - 1) / C::RPL - wave * C::LX;
@@ -216,7 +223,7 @@ struct TileLoader {
     // Byte offset of the lane's piece of load number i of an operand.
     __device__ static __forceinline__ int piece(int i, int lane) {
         const int row = i * C::RPL + lane / C::PIECES;
-        return (lane % C::PIECES) ^ (row & 7);
+        return (lane % C::PIECES) ^ swizzle<C>(row);
     }
     __device__ static __forceinline__ uint32_t offset(int i, int lane, int last, uint32_t rb) {
         const int row = i * C::RPL + lane / C::PIECES;
@@ -285,7 +292,7 @@ __device__ __forceinline__ void tile_steps(const char *buf, f32x4 (&acc)[C::FM][
     const int r = lane & 15;
     const char *px = buf + ((wave % C::NWM) * C::WM + r) * (2 * C::BK);
     const char *pw = buf + C::XBYTES + ((wave / C::NWM) * C::WN + r) * (2 * C::BK);
-    const auto piece = [&](int kk) { return 16 * ((4 * (k0 + kk) + (lane >> 4)) ^ (r & 7)); };
+    const auto piece = [&](int kk) { return 16 * ((4 * (k0 + kk) + (lane >> 4)) ^ swizzle<C>(r)); };
     u32x4 x[RX][G], w[RW][C::FN];
     const auto read = [&](int s) {
         const int kk = s / NG, g = s % NG;
@@ -342,7 +349,7 @@ __global__ __launch_bounds__(64 * C::WAVES) void k_linear_tile(LinearArgs a, int
     if (!tile_of(blockIdx.x, mtiles, ntiles, m0, n0))
         return;
     m0 *= C::BM;
-    n0 *= C::BN;
+    n0 = a.lo + n0 * C::BN;
     const bool loads = C::NL == C::WAVES || wave < C::NL;
     const bool works = C::NW == C::WAVES || wave < C::NW;
     const TileLoader<C> ld(a, m0, n0);
@@ -407,7 +414,7 @@ __global__ __launch_bounds__(64 * C::WAVES) void k_linear_tile(LinearArgs a, int
         for (int e = lane; e < HALF * 16 * (C::WN / 8); e += 64) {
             const int row = e / (C::WN / 8), col = e % (C::WN / 8) * 8;
             const int m = wm + h * HALF * 16 + row, n = wn + col;
-            if (m < a.M && n < a.N) {
+            if (m < a.M && n < a.hi) {
                 const f32x4 v0 = *reinterpret_cast<const f32x4 *>(mine + row * PITCH + col);
                 const f32x4 v1 = *reinterpret_cast<const f32x4 *>(mine + row * PITCH + col + 4);
                 float v[8] = {v0[0], v0[1], v0[2], v0[3], v1[0], v1[1], v1[2], v1[3]};
@@ -422,7 +429,7 @@ __global__ __launch_bounds__(64 * C::WAVES) void k_linear_tile(LinearArgs a, int
 
 // All shapes give the same bits; the choice is for time alone. A shape's time
 // is modelled as that of its rounds of tiles over the 256 compute units. A
-// round takes fix (us) + K ns, measured at K = 1024 and 4096 with one workgroup
+// round takes fix (us) + K ns, measured (random data) at K = 1024 and 4096 with one workgroup
 // on each compute unit (fix1, ns1) and with as many as fit (fix, ns); in
 // between by the line through the two.
 struct Shape {
@@ -443,67 +450,106 @@ inline float shape_time(const Shape &s, int64_t M, int64_t N, int64_t K) {
     return t;
 }
 
-template <int N>
-int best_shape(const Shape (&s)[N], const LinearArgs &a) {
+template <int S>
+int best_shape(const Shape (&s)[S], int64_t M, int64_t N, int64_t K, float *time) {
     int best = 0;
-    float least = shape_time(s[0], a.M, a.N, a.K);
-    for (int i = 1; i < N; ++i) {
-        const float t = shape_time(s[i], a.M, a.N, a.K);
-        if (t < least) {
-            least = t;
+    *time = shape_time(s[0], M, N, K);
+    for (int i = 1; i < S; ++i) {
+        const float t = shape_time(s[i], M, N, K);
+        if (t < *time) {
+            *time = t;
             best = i;
         }
     }
     return best;
 }
 
+// One launch over all columns, or one over the columns of a shape's whole rounds
+// and one, in a smaller shape, over the rest, where the last round would leave
+// most of the device idle (8192 x 10304 x 2048 in 256 x 256 tiles: 5 rounds and 32
+// tiles, 386 us; with the last 64 columns on their own 305). `each` launches
+// the shape it is given over the columns of its arguments.
+constexpr float kSecondLaunch = 2.0f;
+template <int S, class F>
+hipError_t by_columns(const Shape (&s)[S], LinearArgs a, F each) {
+    float best, rest_time;
+    int first = best_shape(s, a.M, a.N, a.K, &best), second = 0;
+    int64_t n1 = a.N;
+    for (int i = 0; i < S; ++i) {
+        const int64_t mt = (a.M + s[i].bm - 1) / s[i].bm, nt = (a.N + s[i].bn - 1) / s[i].bn;
+        const int64_t round = kUnits * s[i].fit, cols = mt * nt / round * round / mt * s[i].bn;
+        if (cols <= 0 || cols >= a.N)
+            continue;
+        const int j = best_shape(s, a.M, a.N - cols, a.K, &rest_time);
+        const float t = shape_time(s[i], a.M, cols, a.K) + rest_time + kSecondLaunch;
+        if (t < best) {
+            best = t;
+            first = i;
+            second = j;
+            n1 = cols;
+        }
+    }
+    a.lo = 0;
+    a.hi = (int32_t)n1;
+    const hipError_t e = each(first, a);
+    if (e != hipSuccess || n1 == a.N)
+        return e;
+    a.lo = (int32_t)n1;
+    a.hi = a.N;
+    return each(second, a);
+}
+
 template <class C>
 hipError_t launch_tile(const LinearArgs &a, hipStream_t stream) {
-    const int64_t mt = (a.M + C::BM - 1) / C::BM, nt = (a.N + C::BN - 1) / C::BN;
+    const int64_t mt = (a.M + C::BM - 1) / C::BM, nt = (a.hi - a.lo + C::BN - 1) / C::BN;
     // (a multiple of 8: runs of tiles for the XCDs)
     const dim3 grid((unsigned)((mt * nt + 7) / 8 * 8));
     k_linear_tile<C><<<grid, dim3(64 * C::WAVES), 0, stream>>>(a, (int)mt, (int)nt);
     return hipGetLastError();
 }
 
-hipError_t linear_bf16(const LinearArgs &a, hipStream_t stream) {
+hipError_t linear_bf16(const LinearArgs &args, hipStream_t stream) {
     static constexpr Shape kShapes[] = {
         {16, 16, 3, 0.0f, 1.6f, 0.0f, 3.4f},       {16, 16, 1, 0.5f, 1.0f, 0.5f, 1.0f},
         {32, 32, 2, 0.5f, 2.3f, 0.5f, 3.0f},       {64, 32, 1, 0.2f, 2.9f, 0.2f, 2.9f},
-        {64, 64, 2, 1.0f, 4.1f, 1.0f, 5.6f},       {128, 64, 2, 1.3f, 5.0f, 2.8f, 7.9f},
-        {128, 128, 2, 4.3f, 8.9f, 5.2f, 10.7f},    {256, 256, 1, 10.0f, 20.6f, 10.0f, 20.6f},
+        {64, 64, 2, 0.9f, 4.2f, 0.7f, 5.8f},       {128, 64, 2, 1.5f, 5.0f, 1.8f, 8.8f},
+        {128, 128, 2, 4.5f, 8.9f, 3.4f, 13.2f},    {256, 256, 1, 8.1f, 23.8f, 8.1f, 23.8f},
     };
-    switch (best_shape(kShapes, a)) {
-    case 0: return launch_tile<Tile<false, 16, 16, 16, 16, 256, 3, 4>>(a, stream);
-    case 1: return launch_tile<Tile<false, 16, 16, 16, 16, 512, 5, 8>>(a, stream);
-    case 2: return launch_tile<Tile<false, 32, 32, 16, 16, 128, 4>>(a, stream);
-    case 3: return launch_tile<Tile<false, 64, 32, 32, 16, 256, 3>>(a, stream);
-    case 4: return launch_tile<Tile<false, 64, 64, 32, 32, 64, 4>>(a, stream);
-    case 5: return launch_tile<Tile<false, 128, 64, 32, 32, 64, 3>>(a, stream);
-    case 6: return launch_tile<Tile<false, 128, 128, 32, 64, 64, 2>>(a, stream);
-    default: return launch_tile<Tile<false, 256, 256, 128, 64, 64, 2>>(a, stream);
-    }
+    return by_columns(kShapes, args, [&](int shape, const LinearArgs &a) {
+        switch (shape) {
+        case 0: return launch_tile<Tile<false, 16, 16, 16, 16, 256, 3, 4>>(a, stream);
+        case 1: return launch_tile<Tile<false, 16, 16, 16, 16, 512, 5, 8>>(a, stream);
+        case 2: return launch_tile<Tile<false, 32, 32, 16, 16, 128, 4>>(a, stream);
+        case 3: return launch_tile<Tile<false, 64, 32, 32, 16, 256, 3>>(a, stream);
+        case 4: return launch_tile<Tile<false, 64, 64, 32, 32, 64, 4>>(a, stream);
+        case 5: return launch_tile<Tile<false, 128, 64, 32, 32, 64, 3>>(a, stream);
+        case 6: return launch_tile<Tile<false, 128, 128, 32, 64, 64, 2>>(a, stream);
+        default: return launch_tile<Tile<false, 256, 256, 128, 64, 64, 2>>(a, stream);
+        }
+    });
 }
 
 // fp32 is bound by the matrix instructions from 32 x 32 on (131 of 157 TFLOP/s
 // peak in full rounds): the shapes differ in how evenly the tiles divide.
-hipError_t linear_f32(const LinearArgs &a, hipStream_t stream) {
+hipError_t linear_f32(const LinearArgs &args, hipStream_t stream) {
     static constexpr Shape kShapes[] = {
         {16, 16, 3, 0.0f, 5.8f, 0.4f, 7.4f},       {16, 16, 1, 0.2f, 5.4f, 0.2f, 5.4f},
         {32, 32, 2, 0.4f, 7.4f, 1.1f, 10.2f},      {64, 32, 3, 0.2f, 11.9f, 2.5f, 23.6f},
         {64, 64, 2, 1.1f, 19.4f, 3.0f, 30.3f},     {128, 64, 3, 2.4f, 33.3f, 6.8f, 85.1f},
         {128, 128, 2, 4.8f, 62.5f, 8.4f, 112.0f},  {256, 128, 1, 7.7f, 119.0f, 7.7f, 119.0f},
     };
-    switch (best_shape(kShapes, a)) {
-    case 0: return launch_tile<Tile<true, 16, 16, 16, 16, 256, 3, 4>>(a, stream);
-    case 1: return launch_tile<Tile<true, 16, 16, 16, 16, 512, 5, 8>>(a, stream);
-    case 2: return launch_tile<Tile<true, 32, 32, 16, 16, 128, 4>>(a, stream);
-    case 3: return launch_tile<Tile<true, 64, 32, 32, 16, 128, 2>>(a, stream);
-    case 4: return launch_tile<Tile<true, 64, 64, 32, 32, 128, 2>>(a, stream);
-    case 5: return launch_tile<Tile<true, 128, 64, 32, 32, 64, 2>>(a, stream);
-    case 6: return launch_tile<Tile<true, 128, 128, 32, 64, 64, 2>>(a, stream);
-    default: return launch_tile<Tile<true, 256, 128, 64, 64, 64, 2>>(a, stream);
-    }
+    return by_columns(kShapes, args, [&](int shape, const LinearArgs &a) {
+        switch (shape) {
+        case 0: return launch_tile<Tile<true, 16, 16, 16, 16, 256, 3, 4>>(a, stream);
+        case 1: return launch_tile<Tile<true, 16, 16, 16, 16, 512, 5, 8>>(a, stream);
+        case 2: return launch_tile<Tile<true, 32, 32, 16, 16, 128, 4>>(a, stream);
+        case 3: return launch_tile<Tile<true, 64, 32, 32, 16, 128, 2>>(a, stream);
+        case 4: return launch_tile<Tile<true, 64, 64, 32, 32, 128, 2>>(a, stream);
+        case 5: return launch_tile<Tile<true, 128, 64, 32, 32, 64, 2>>(a, stream);
+        case 6: return launch_tile<Tile<true, 128, 128, 32, 64, 64, 2>>(a, stream);
+        default: return launch_tile<Tile<true, 256, 128, 64, 64, 64, 2>>(a, stream);
+        }
+    });
 }
 
 }  // namespace

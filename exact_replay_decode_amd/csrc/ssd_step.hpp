@@ -21,6 +21,7 @@ struct LinearSeg {
 
 struct LinearArgs {
     int32_t M, N, K;
+    int32_t lo, hi;           // columns of this launch (set by the launcher), lo % 16 == 0
     int32_t io_bf16;
     int32_t act;              // ssd_activation
     const void *x, *w;        // [M,K], [N,K]
