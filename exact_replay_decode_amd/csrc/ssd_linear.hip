@@ -152,17 +152,22 @@ typedef __attribute__((address_space(3))) void lds_void;
 // WM x WN each (16 x 16 tiles). Both operands pass through LDS in tiles of 2 BK
 // bytes of k (BK bf16, BK / 2 fp32), S buffers in turn: the direct loads (global_load_lds, 16 bytes a lane) of the
 // S - 1 tiles ahead run while the matrix cores work on this one. NL waves issue
-// the loads (more than compute, where one tile is all the work of a group).
+// the loads; with APART waves of their own, where a compute unit has one small
+// tile and the issue of the loads would hold up its few MFMAs (256 x 2048 x 4096 in
+// 64 x 32 tiles: 15.5 us, 12.8 with eight loading waves, 11.6 with four apart).
 // LDS layout: row r of a tile at 2 BK r bytes, its 16-byte piece c at c ^ (r % 8),
 // so that the 16 rows that a fragment read touches spread over the banks. A
 // direct load fills 1 KB in lane order, whole rows or more, so a lane fetches
 // the piece that belongs at its place.
-template <bool F32_, int BM_, int BN_, int WM_, int WN_, int BK_, int S_, int NL_ = 0>
+template <bool F32_, int BM_, int BN_, int WM_, int WN_, int BK_, int S_, int NL_ = 0,
+          bool APART = false>
 struct Tile {
     static constexpr bool F32 = F32_;
     static constexpr int BM = BM_, BN = BN_, WM = WM_, WN = WN_, BK = BK_, S = S_;
     static constexpr int NWM = BM / WM, NWN = BN / WN, NW = NWM * NWN;
-    static constexpr int NL = NL_ ? NL_ : NW, WAVES = NL > NW ? NL : NW;
+    static constexpr int NL = NL_ ? NL_ : NW;
+    static constexpr int L0 = APART ? NW : 0;             // the first wave that loads
+    static constexpr int WAVES = L0 + NL > NW ? L0 + NL : NW;
     static constexpr int FM = WM / 16, FN = WN / 16;
     static constexpr int PIECES = BK / 8;                 // 16-byte pieces of a row
     static constexpr int RPL = 64 / PIECES;               // rows of one direct load
@@ -205,7 +210,7 @@ struct TileLoader {
     uint32_t lx, lw;                  // LDS offsets of the wave's loads in a buffer
     int nx;                           // loads of x that hold rows below M
     __device__ __forceinline__ TileLoader(const LinearArgs &a, int m0, int n0) {
-        const int lane = threadIdx.x & 63, wave = wave_id();
+        const int lane = threadIdx.x & 63, wave = wave_id() - C::L0;
         const uint32_t rb = row_bytes(a);
         x = static_cast<const char *>(a.x) + (int64_t)m0 * rb;
         w = static_cast<const char *>(a.w) + (int64_t)n0 * rb;
@@ -248,7 +253,7 @@ struct TileLoader {
     // The last tile when 2 BK does not divide a row: pieces past it are zeros
     // (left: what is there, in units of 2 bytes).
     __device__ __forceinline__ void load_tail(char *buf, int64_t kb, int left) const {
-        const int lane = threadIdx.x & 63, wave = wave_id();
+        const int lane = threadIdx.x & 63, wave = wave_id() - C::L0;
         const u32x4 zero = {0, 0, 0, 0};
 #pragma unroll
         for (int i = 0; i < C::LX; ++i)
@@ -350,7 +355,7 @@ __global__ __launch_bounds__(64 * C::WAVES) void k_linear_tile(LinearArgs a, int
         return;
     m0 *= C::BM;
     n0 = a.lo + n0 * C::BN;
-    const bool loads = C::NL == C::WAVES || wave < C::NL;
+    const bool loads = C::NL == C::WAVES || (wave >= C::L0 && wave < C::L0 + C::NL);
     const bool works = C::NW == C::WAVES || wave < C::NW;
     const TileLoader<C> ld(a, m0, n0);
     f32x4 acc[C::FM][C::FN] = {};
@@ -510,20 +515,22 @@ hipError_t launch_tile(const LinearArgs &a, hipStream_t stream) {
 
 hipError_t linear_bf16(const LinearArgs &args, hipStream_t stream) {
     static constexpr Shape kShapes[] = {
-        {16, 16, 3, 0.0f, 1.6f, 0.0f, 3.4f},       {16, 16, 1, 0.5f, 1.0f, 0.5f, 1.0f},
-        {32, 32, 2, 0.5f, 2.3f, 0.5f, 3.0f},       {64, 32, 1, 0.2f, 2.9f, 0.2f, 2.9f},
-        {64, 64, 2, 0.9f, 4.2f, 0.7f, 5.8f},       {128, 64, 2, 1.5f, 5.0f, 1.8f, 8.8f},
-        {128, 128, 2, 4.5f, 8.9f, 3.4f, 13.2f},    {256, 256, 1, 8.1f, 23.8f, 8.1f, 23.8f},
+        {16, 16, 3, 0.0f, 1.6f, 0.0f, 3.4f},     {16, 16, 2, 0.3f, 1.06f, 0.8f, 2.5f},
+        {32, 32, 2, 0.3f, 1.6f, 0.3f, 2.7f},     {64, 32, 1, 0.7f, 2.07f, 0.7f, 2.07f},
+        {64, 64, 2, 0.9f, 4.2f, 0.7f, 5.8f},     {64, 64, 1, 1.2f, 3.13f, 1.2f, 3.13f},
+        {128, 64, 2, 1.5f, 5.0f, 1.8f, 8.8f},    {128, 128, 2, 4.5f, 8.9f, 3.4f, 13.2f},
+        {256, 256, 1, 8.1f, 23.8f, 8.1f, 23.8f},
     };
     return by_columns(kShapes, args, [&](int shape, const LinearArgs &a) {
         switch (shape) {
         case 0: return launch_tile<Tile<false, 16, 16, 16, 16, 256, 3, 4>>(a, stream);
-        case 1: return launch_tile<Tile<false, 16, 16, 16, 16, 512, 5, 8>>(a, stream);
-        case 2: return launch_tile<Tile<false, 32, 32, 16, 16, 128, 4>>(a, stream);
-        case 3: return launch_tile<Tile<false, 64, 32, 32, 16, 256, 3>>(a, stream);
+        case 1: return launch_tile<Tile<false, 16, 16, 16, 16, 256, 4, 8, true>>(a, stream);
+        case 2: return launch_tile<Tile<false, 32, 32, 16, 16, 256, 2, 4, true>>(a, stream);
+        case 3: return launch_tile<Tile<false, 64, 32, 16, 32, 256, 3, 4, true>>(a, stream);
         case 4: return launch_tile<Tile<false, 64, 64, 32, 32, 64, 4>>(a, stream);
-        case 5: return launch_tile<Tile<false, 128, 64, 32, 32, 64, 3>>(a, stream);
-        case 6: return launch_tile<Tile<false, 128, 128, 32, 64, 64, 2>>(a, stream);
+        case 5: return launch_tile<Tile<false, 64, 64, 32, 32, 128, 4, 4, true>>(a, stream);
+        case 6: return launch_tile<Tile<false, 128, 64, 32, 32, 64, 3>>(a, stream);
+        case 7: return launch_tile<Tile<false, 128, 128, 32, 64, 64, 2>>(a, stream);
         default: return launch_tile<Tile<false, 256, 256, 128, 64, 64, 2>>(a, stream);
         }
     });
@@ -533,20 +540,22 @@ hipError_t linear_bf16(const LinearArgs &args, hipStream_t stream) {
 // peak in full rounds): the shapes differ in how evenly the tiles divide.
 hipError_t linear_f32(const LinearArgs &args, hipStream_t stream) {
     static constexpr Shape kShapes[] = {
-        {16, 16, 3, 0.0f, 5.8f, 0.4f, 7.4f},       {16, 16, 1, 0.2f, 5.4f, 0.2f, 5.4f},
-        {32, 32, 2, 0.4f, 7.4f, 1.1f, 10.2f},      {64, 32, 3, 0.2f, 11.9f, 2.5f, 23.6f},
-        {64, 64, 2, 1.1f, 19.4f, 3.0f, 30.3f},     {128, 64, 3, 2.4f, 33.3f, 6.8f, 85.1f},
-        {128, 128, 2, 4.8f, 62.5f, 8.4f, 112.0f},  {256, 128, 1, 7.7f, 119.0f, 7.7f, 119.0f},
+        {16, 16, 3, 0.0f, 5.8f, 0.4f, 7.3f},     {16, 16, 1, 0.2f, 5.35f, 0.2f, 5.35f},
+        {32, 32, 2, 0.3f, 5.8f, 1.5f, 8.75f},    {64, 32, 3, 0.3f, 11.5f, 2.0f, 23.6f},
+        {64, 32, 1, 0.9f, 9.4f, 0.9f, 9.4f},     {64, 64, 2, 1.2f, 19.2f, 2.9f, 29.5f},
+        {128, 64, 3, 2.5f, 33.2f, 5.7f, 85.0f},  {128, 128, 2, 5.4f, 62.0f, 7.8f, 112.6f},
+        {256, 128, 1, 7.4f, 119.0f, 7.4f, 119.0f},
     };
     return by_columns(kShapes, args, [&](int shape, const LinearArgs &a) {
         switch (shape) {
         case 0: return launch_tile<Tile<true, 16, 16, 16, 16, 256, 3, 4>>(a, stream);
         case 1: return launch_tile<Tile<true, 16, 16, 16, 16, 512, 5, 8>>(a, stream);
-        case 2: return launch_tile<Tile<true, 32, 32, 16, 16, 128, 4>>(a, stream);
+        case 2: return launch_tile<Tile<true, 32, 32, 16, 16, 256, 2, 8, true>>(a, stream);
         case 3: return launch_tile<Tile<true, 64, 32, 32, 16, 128, 2>>(a, stream);
-        case 4: return launch_tile<Tile<true, 64, 64, 32, 32, 128, 2>>(a, stream);
-        case 5: return launch_tile<Tile<true, 128, 64, 32, 32, 64, 2>>(a, stream);
-        case 6: return launch_tile<Tile<true, 128, 128, 32, 64, 64, 2>>(a, stream);
+        case 4: return launch_tile<Tile<true, 64, 32, 32, 16, 256, 3, 4, true>>(a, stream);
+        case 5: return launch_tile<Tile<true, 64, 64, 32, 32, 128, 2>>(a, stream);
+        case 6: return launch_tile<Tile<true, 128, 64, 32, 32, 64, 2>>(a, stream);
+        case 7: return launch_tile<Tile<true, 128, 128, 32, 64, 64, 2>>(a, stream);
         default: return launch_tile<Tile<true, 256, 128, 64, 64, 64, 2>>(a, stream);
         }
     });
