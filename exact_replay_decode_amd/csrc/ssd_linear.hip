@@ -250,21 +250,35 @@ struct TileLoader {
         for (int i = 0; i < C::LW; ++i)
             direct_load(lds + lw + 1024 * i, w + kb, ow[i]);
     }
-    // The last tile when 2 BK does not divide a row: pieces past it are zeros
-    // (left: what is there, in units of 2 bytes).
+    // The last tile when 2 BK does not divide a row (left: what is there, in units
+    // of 2 bytes): pieces past the row fetch the tile's first piece instead ...
     __device__ __forceinline__ void load_tail(char *buf, int64_t kb, int left) const {
+        const int lane = threadIdx.x & 63, wave = wave_id() - C::L0;
+        const uint32_t lds = (uint32_t)(uintptr_t)(lds_void *)buf;
+        const auto at = [&](uint32_t off, int i) {
+            const int p = piece(i, lane);
+            return 8 * p < left ? off : off - 16 * p;
+        };
+#pragma unroll
+        for (int i = 0; i < C::LX; ++i)
+            if (C::BM > 32 || i < nx)
+                direct_load(lds + lx + 1024 * i, x + kb, at(ox[i], wave * C::LX + i));
+#pragma unroll
+        for (int i = 0; i < C::LW; ++i)
+            direct_load(lds + lw + 1024 * i, w + kb, at(ow[i], wave * C::LW + i));
+    }
+    // ... and, once there, become zeros.
+    __device__ __forceinline__ void zero_tail(char *buf, int left) const {
         const int lane = threadIdx.x & 63, wave = wave_id() - C::L0;
         const u32x4 zero = {0, 0, 0, 0};
 #pragma unroll
         for (int i = 0; i < C::LX; ++i)
-            *reinterpret_cast<u32x4 *>(buf + lx + 1024 * i + 16 * lane) =
-                8 * piece(wave * C::LX + i, lane) < left
-                    ? *reinterpret_cast<const u32x4 *>(x + kb + ox[i]) : zero;
+            if (8 * piece(wave * C::LX + i, lane) >= left)
+                *reinterpret_cast<u32x4 *>(buf + lx + 1024 * i + 16 * lane) = zero;
 #pragma unroll
         for (int i = 0; i < C::LW; ++i)
-            *reinterpret_cast<u32x4 *>(buf + lw + 1024 * i + 16 * lane) =
-                8 * piece(wave * C::LW + i, lane) < left
-                    ? *reinterpret_cast<const u32x4 *>(w + kb + ow[i]) : zero;
+            if (8 * piece(wave * C::LW + i, lane) >= left)
+                *reinterpret_cast<u32x4 *>(buf + lw + 1024 * i + 16 * lane) = zero;
     }
 };
 
@@ -360,40 +374,46 @@ __global__ __launch_bounds__(64 * C::WAVES) void k_linear_tile(LinearArgs a, int
     const TileLoader<C> ld(a, m0, n0);
     f32x4 acc[C::FM][C::FN] = {};
     const int k2 = a.K * (C::F32 ? 2 : 1);   // a row in units of 2 bytes
-    const int full = k2 / BK, left = k2 % BK;
+    const int full = k2 / BK, left = k2 % BK, tiles = full + (left != 0);
+    const auto load = [&](int t, int slot) {
+        if (t < full)
+            ld.load(buf + slot * C::BYTES, (int64_t)t * BK * 2);
+        else
+            ld.load_tail(buf + slot * C::BYTES, (int64_t)t * BK * 2, left);
+    };
 #pragma unroll
     for (int t = 0; t < S - 1; ++t)
-        if (t < full && loads)
-            ld.load(buf + t * C::BYTES, t * BK * 2);
+        if (t < tiles && loads)
+            load(t, t);
     int slot = 0, ahead = S - 1;      // t % S and (t + S - 1) % S
     for (int t = 0; t < full; ++t) {
         // tile t is there when only the loads of the S - 2 tiles after it are in
         // flight (with loads left out fewer: that waits for more); past the
         // barrier every wave has read tile t - 1, whose buffer is loaded next
-        if (C::BM > 32 && t + S - 2 < full)
+        if (C::BM > 32 && t + S - 2 < tiles)
             loads_barrier<(S - 2) * (C::LX + C::LW)>();
-        else if (t + S - 2 < full)
+        else if (t + S - 2 < tiles)
             loads_barrier<(S - 2) * C::LW>();
         else
             loads_barrier<0>();
-        if (t + S - 1 < full && loads)
-            ld.load(buf + ahead * C::BYTES, (int64_t)(t + S - 1) * BK * 2);
+        if (t + S - 1 < tiles && loads)
+            load(t + S - 1, ahead);
         if (works)
             tile_steps<C, BK / 32>(buf + slot * C::BYTES, acc);
         slot = slot + 1 == S ? 0 : slot + 1;
         ahead = ahead + 1 == S ? 0 : ahead + 1;
     }
-    __syncthreads();
     if (left) {
+        loads_barrier<0>();
         if (loads)
-            ld.load_tail(buf, (int64_t)full * BK * 2, left);
+            ld.zero_tail(buf + slot * C::BYTES, left);
         __syncthreads();
         if (works)
 #pragma unroll 1
             for (int k = 0; k < left; k += 32)
-                tile_steps<C, 1>(buf, acc, k / 32);
-        __syncthreads();
+                tile_steps<C, 1>(buf + slot * C::BYTES, acc, k / 32);
     }
+    __syncthreads();
     if (!works)
         return;
     // Epilogue through LDS, 32 of the wave's rows at a time in its own part of
