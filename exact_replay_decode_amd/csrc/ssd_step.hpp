@@ -31,6 +31,10 @@ struct LinearArgs {
     LinearSeg seg[3];
 };
 
+// Tiles of a product's launch at most: its threads (up to 576 a tile) are counted
+// in 32 bits. A size whose 128 x 128 tiles are no more than this has a kernel.
+constexpr int64_t kLinearMaxTiles = 1 << 22;
+
 struct NormArgs {
     int64_t T;
     int32_t C, gs;            // channels of a row, channels of a group

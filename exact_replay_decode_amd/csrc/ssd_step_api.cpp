@@ -17,6 +17,8 @@ using ssd::Dims;
 
 constexpr int64_t kMaxI32 = std::numeric_limits<int32_t>::max();
 constexpr int32_t kMaxPages = 1 << 20;
+constexpr int64_t kMaxElems = (int64_t)1 << 34;   // of a norm
+constexpr int32_t kMaxList = (1 << 24) - 8;       // rows or entries with 256 threads each
 
 bool known_dtype(int dt) { return dt == SSD_F32 || dt == SSD_BF16; }
 bool natural(const void *p, int dt) { return (uintptr_t)p % dtype_bytes(dt) == 0; }
@@ -32,8 +34,7 @@ int check_linear(int64_t M, int64_t N, int64_t K, int32_t io) {
     if (M > kMaxI32 - 65536 || N > kMaxI32 - 65536 || K > (1 << 20) ||
         K % (io == SSD_BF16 ? 8 : 4) != 0)
         return SSD_ERR_UNSUPPORTED;
-    // 16 x 16 tiles, the smallest unit of a launch, within one grid dimension
-    if (((M + 15) / 16) * ((N + 15) / 16) > kMaxI32 - 8)
+    if (((M + 127) / 128) * ((N + 127) / 128) > ssd::kLinearMaxTiles)
         return SSD_ERR_UNSUPPORTED;
     return SSD_OK;
 }
@@ -162,7 +163,8 @@ int ssd_gated_norm(const ssd_shape *sh, int64_t T, int32_t groups, float eps,
     if (T < 0 || groups < 1 || d.H % groups != 0 || !(eps >= 0.0f) || std::isinf(eps))
         return SSD_ERR_SHAPE;
     const int64_t C = (int64_t)d.H * d.P, gs = C / groups;
-    if (gs > 32768 || T > kMaxI32 / groups)
+    // (at most a thread for four channels, whose number is one of 32 bits)
+    if (gs > 32768 || T > kMaxElems / C)
         return SSD_ERR_UNSUPPORTED;
     if (T == 0)
         return SSD_OK;
@@ -191,8 +193,8 @@ int ssd_token_logprobs(int64_t T, int64_t V, int32_t dtype, const void *logits,
         return SSD_ERR_DTYPE;
     if (T < 0 || V < 1 || top_k < 0 || top_k > V)
         return SSD_ERR_SHAPE;
-    // (indices up to a chunk past V stay within 32 bits)
-    if (T > kMaxI32 || V > kMaxI32 - 65536 || top_k > 64)
+    // (indices up to a chunk past V stay within 32 bits, as do 256 threads a row)
+    if (T > kMaxList || V > kMaxI32 - 65536 || top_k > 64)
         return SSD_ERR_UNSUPPORTED;
     if (T == 0)
         return SSD_OK;
@@ -271,6 +273,8 @@ int ssd_replay_cache_free(const ssd_shape *sh, const ssd_replay_cache *cache, in
         return st;
     if (n < 0 || (!slot_idx && n > cache->num_slots))
         return SSD_ERR_SHAPE;
+    if (n > kMaxList)
+        return SSD_ERR_UNSUPPORTED;
     if (n == 0)
         return SSD_OK;
     if ((st = check_slots_distinct(slot_idx, n, cache->num_slots)) != SSD_OK)
@@ -292,6 +296,8 @@ int ssd_replay_cache_copy(const ssd_shape *sh, const ssd_replay_cache *dst,
         return st;
     if (n < 0)
         return SSD_ERR_SHAPE;
+    if (n > kMaxList)
+        return SSD_ERR_UNSUPPORTED;
     if (n == 0)
         return SSD_OK;
     if (!dst_idx || !src_idx || (dst->buf_C && !src->buf_C))

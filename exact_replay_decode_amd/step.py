@@ -67,17 +67,17 @@ def _p(t):
 
 def _shape(shape):
     """The C struct of a Shape by reference, made once per object."""
-    ref = shape.__dict__.get("_ref")
-    if ref is None:
-        ref = ctypes.byref(shape.c())
-        object.__setattr__(shape, "_ref", ref)   # (no field: not compared, not hashed)
-    return ref
+    c = shape.__dict__.get("_c")
+    if c is None:
+        c = shape.c()   # (no field: not compared, not hashed; copied and pickled as the rest)
+        object.__setattr__(shape, "_c", c)
+    return ctypes.byref(c)
 
 
 def ssd_linear(x, weight, bias=None, activation="none", residual=None, out=None, out_dtype=None,
                stream=None):
-    """act(x @ weight.T + bias) + residual in one launch: x [M, K], weight
-    [N, K], residual [M, N] of one dtype (bf16 or fp32), bias [N] fp32; K a
+    """act(x @ weight.T + bias) + residual, fused: x [M, K], weight [N, K],
+    residual [M, N] of one dtype (bf16 or fp32), bias [N] fp32; K a
     multiple of 8 (bf16) or 4 (fp32). activation: none, silu, gelu (tanh form)
     or relu2. out [M, N] in out_dtype (x's by default; bf16 or fp32); out may
     be the residual. A row's bits do not depend on M."""
@@ -111,7 +111,7 @@ def ssd_linear(x, weight, bias=None, activation="none", residual=None, out=None,
 
 
 def ssd_in_proj(shape: Shape, u, weight, bias=None, out=None, stream=None):
-    """The mixer's in-projection in one launch: u [M, d_model] with weight
+    """The mixer's in-projection: u [M, d_model] with weight
     [2*H*P + 2*G*N + H, d_model] (bias fp32 or None). Returns z [M, H, P], xBC
     [M, conv_dim] and raw dt [M, H], the arrays the gate, the conv and the
     scan take; out: the three to write into."""

@@ -41,9 +41,10 @@ typedef enum {
  * The sum is one fp32 chain over k in a fixed order (matrix-core steps of 32
  * k in bf16, of 4 in fp32; a bf16 product is exact in fp32), the epilogue is
  * fp32, and the result is rounded once. The bits of a row do not depend on M.
- * M >= 0, N >= 0, K >= 1; K a multiple of 8 (bf16) or 4 (fp32) and at most
- * 1048576, else SSD_ERR_UNSUPPORTED; x and w 16-byte aligned (the others need their natural
- * alignment). */
+ * M >= 0, N >= 0, K >= 1. K a multiple of 8 (bf16) or 4 (fp32) and at most
+ * 1048576, and at most 4194304 tiles of 128 x 128 outputs, else
+ * SSD_ERR_UNSUPPORTED. x and w 16-byte aligned (the others need their natural
+ * alignment). One launch, or two over the columns. */
 int ssd_linear(int64_t M, int64_t N, int64_t K, int32_t io_dtype,
                int32_t out_dtype, int32_t activation, const void *x,
                const void *w, const float *bias, const void *residual,
@@ -68,8 +69,9 @@ int ssd_in_proj(const ssd_shape *shape, int64_t M, int64_t d_model,
  *   y, z  [T,H,P] io_dtype; z NULL: no gate
  *   w     [H*P] fp32
  *   out   [T,H,P] io_dtype; may be y or z itself
- * fp32 inside, rounded once. groups divides H; gs at most 32768, else
- * SSD_ERR_UNSUPPORTED; eps >= 0 and finite, else SSD_ERR_SHAPE. */
+ * fp32 inside, rounded once. groups divides H; gs at most 32768 and T*H*P at
+ * most 2^34, else SSD_ERR_UNSUPPORTED; eps >= 0 and finite, else
+ * SSD_ERR_SHAPE. All arrays 16-byte aligned. */
 int ssd_gated_norm(const ssd_shape *shape, int64_t T, int32_t groups, float eps,
                    int32_t norm_before_gate, const void *y, const void *z,
                    const float *w, void *out, hipStream_t stream);
@@ -90,8 +92,8 @@ int ssd_gated_norm(const ssd_shape *shape, int64_t T, int32_t groups, float eps,
  * -inf) has logprob and top_logprobs -inf, entropy 0, and ranks by index. A
  * row that holds a NaN or +inf has no distribution: logprob, entropy and
  * top_logprobs are NaN, rank and top_ids -1.
- * T >= 0, 1 <= V < 2^31, 0 <= top_k <= min(64, V). One launch, no workspace;
- * sums in fp32 over a fixed split of the row. */
+ * 0 <= T <= 16777208, 1 <= V < 2^31 - 65536, 0 <= top_k <= min(64, V). One
+ * launch, no workspace; sums in fp32 over a fixed split of the row. */
 int ssd_token_logprobs(int64_t T, int64_t V, int32_t dtype, const void *logits,
                        const int32_t *tokens, int32_t top_k, float *logprob,
                        float *entropy, int32_t *rank, int32_t *top_ids,
@@ -105,8 +107,11 @@ int ssd_token_logprobs(int64_t T, int64_t V, int32_t dtype, const void *logits,
  * page". Nothing else is kept between calls, so a table that the caller
  * edits stays right. Slot lists must be distinct unless stated, list entries
  * outside [0, num_slots) are skipped. cache->work is not used (may be NULL).
- * num_pages at most 1048576 and num_slots * Q / page_tokens below 2^31
- * (SSD_ERR_UNSUPPORTED). A contiguous cache (buf_pages NULL) is
+ * num_pages at most 1048576, num_slots * Q / page_tokens below 2^31 and lists
+ * of copy and free up to 16777208 entries (SSD_ERR_UNSUPPORTED). One table may
+ * serve the caches of several layers (reserve and trim through any one of
+ * them, copy and free each), but not a pool that is compacted, since that
+ * moves one cache's pages. A contiguous cache (buf_pages NULL) is
  * SSD_ERR_NULL for the page calls and fine for copy and free.
  * Calls on one cache must be ordered (one stream, or events). */
 

@@ -3,8 +3,11 @@ library exports what the header declares, and bad arguments are refused with
 the documented status before anything is launched (fake device pointers; no
 GPU needed). An accepted call would need one, so every call here is refused
 or has nothing to do."""
+import copy
 import ctypes
+import dataclasses
 import os
+import pickle
 import re
 
 import pytest
@@ -53,6 +56,7 @@ def linear(M=4, N=8, K=16, io=BF16, out=BF16, act=0, x=A, w=A, bias=None, res=No
     (dict(M=-1), SHAPE), (dict(N=-1), SHAPE), (dict(K=0), SHAPE), (dict(K=-8), SHAPE),
     (dict(K=12), UNSUP), (dict(io=F32, out=F32, K=6), UNSUP), (dict(K=4), UNSUP),
     (dict(M=2 ** 31), UNSUP), (dict(N=2 ** 31), UNSUP), (dict(M=2 ** 30, N=2 ** 30), UNSUP),
+    (dict(M=2 ** 18, N=2 ** 18 + 1), UNSUP), (dict(N=2 ** 29 + 1), UNSUP),
     (dict(K=2 ** 20 + 8), UNSUP), (dict(io=2), DTYPE), (dict(out=-1), DTYPE),
     (dict(act=4), UNSUP), (dict(act=-1), UNSUP), (dict(x=None), NULL), (dict(w=None), NULL),
     (dict(o=None), NULL), (dict(x=A + 8), ALIGN), (dict(w=A + 2), ALIGN),
@@ -84,7 +88,7 @@ def test_in_proj_refusals(kw, skw, code):
     (dict(eps=float("inf")), {}, SHAPE), (dict(y=None), {}, NULL), (dict(w=None), {}, NULL),
     (dict(o=None), {}, NULL), (dict(z=A + 8), {}, ALIGN), (dict(w=A + 4), {}, ALIGN),
     (dict(groups=1), dict(H=512, G=1, P=128), UNSUP),    # a group of 65536 channels
-    (dict(T=2 ** 31), {}, UNSUP), (dict(T=0, y=None), {}, OK)])
+    (dict(T=2 ** 31), {}, UNSUP), (dict(T=2 ** 28 + 1), {}, UNSUP), (dict(T=0, y=None), {}, OK)])
 def test_gated_norm_refusals(kw, skw, code):
     a = dict(T=4, groups=2, eps=1e-5, y=A, z=None, w=A, o=A)
     a.update(kw)
@@ -95,7 +99,7 @@ def test_gated_norm_refusals(kw, skw, code):
 @pytest.mark.parametrize("kw,code", [
     (dict(T=-1), SHAPE), (dict(V=0), SHAPE), (dict(k=-1), SHAPE), (dict(k=11), SHAPE),
     (dict(V=100, k=65), UNSUP), (dict(V=2 ** 31 - 1), UNSUP), (dict(T=2 ** 31), UNSUP),
-    (dict(dt=3), DTYPE), (dict(x=None), NULL), (dict(tok=None), NULL), (dict(lp=None), NULL),
+    (dict(T=2 ** 24 - 7), UNSUP), (dict(dt=3), DTYPE), (dict(x=None), NULL), (dict(tok=None), NULL), (dict(lp=None), NULL),
     (dict(k=1, ids=None), NULL), (dict(k=1, tlp=None), NULL), (dict(x=A + 1), ALIGN),
     (dict(x=A + 2, dt=F32), ALIGN), (dict(T=0, x=None), OK)])
 def test_token_logprobs_refusals(kw, code):
@@ -165,3 +169,23 @@ def test_binding_refuses_cpu_tensors():
         erd.ssd_token_logprobs(x, x)
     with pytest.raises(TypeError, match="must be a torch.Tensor"):
         erd.ssd_linear(None, x)
+
+
+def test_lists_too_long_for_a_launch_are_refused():
+    lib, sh, c = _lib.load(), ctypes.byref(shape()), ctypes.byref(cache())
+    n = 2 ** 24 - 7
+    assert lib.ssd_replay_cache_free(sh, c, n, A, None) == UNSUP
+    assert lib.ssd_replay_cache_copy(sh, c, c, n, A, A, None, None) == UNSUP
+
+
+def test_a_shape_that_was_used_still_copies_and_pickles():
+    """What the binding keeps with a Shape is no part of its value."""
+    from exact_replay_decode_amd import step
+    sh = erd.Shape(4, 2, 16, 16, 64)
+    step._shape(sh)
+    for other in (copy.copy(sh), copy.deepcopy(sh), pickle.loads(pickle.dumps(sh)),
+                  dataclasses.replace(sh)):
+        assert other == sh and hash(other) == hash(sh) and repr(other) == repr(sh)
+        assert bytes(step._shape(other)._obj) == bytes(sh.c())
+    more = dataclasses.replace(sh, H=8)
+    assert more != sh and step._shape(more)._obj.H == 8
