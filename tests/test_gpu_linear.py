@@ -29,6 +29,54 @@ def test_linear_whole_numbers_are_exact(M, N, K, io):
     assert torch.equal(y.cpu().double(), x.cpu().double() @ w.cpu().double().t())
 
 
+# Sizes of every tile, alone and as the first or the second of two launches over the
+# columns, most with a partial last tile of k.
+TILES = [(1, 17, 1000), (1, 4100, 40), (1, 4100, 136), (33, 4100, 40), (33, 4100, 136),
+         (33, 4100, 520), (1, 16001, 40), (1, 16001, 4104), (65, 8200, 40), (65, 8200, 2056),
+         (65, 16001, 136), (200, 8200, 520), (257, 10300, 40), (513, 10300, 264),
+         (1025, 6001, 40), (2049, 6001, 264), (33, 33000, 520), (33, 33000, 1000),
+         (65, 4100, 4104), (200, 8200, 1000), (65, 33000, 520), (129, 33000, 264),
+         (400, 33000, 264), (700, 16001, 520), (2049, 4100, 520), (2049, 10300, 520),
+         (4097, 1000, 520), (200, 33000, 40), (700, 8200, 40), (4097, 2000, 40),
+         (513, 33000, 136)]
+
+
+@pytest.mark.parametrize("M,N,K", TILES)
+@pytest.mark.parametrize("io", ["bf16", "f32"])
+def test_every_tile_is_exact_in_whole_numbers(M, N, K, io):
+    g = gen(M + N + K)
+    x = torch.randint(-4, 5, (M, K), generator=g, device=DEV).to(DT[io])
+    w = torch.randint(-4, 5, (N, K), generator=g, device=DEV).to(DT[io])
+    y = erd.ssd_linear(x, w, out_dtype=torch.float32)
+    assert torch.equal(y.double(), x.double() @ w.double().t())
+
+
+@pytest.mark.parametrize("M,N,K", [(200, 8200, 1000), (2049, 4100, 520), (400, 33000, 264)])
+@pytest.mark.parametrize("io", ["bf16", "f32"])
+def test_columns_of_two_launches(M, N, K, io):
+    """Bias, activation and residual where the columns are two launches: the
+    bits of the same columns in calls of their own."""
+    g = gen(N)
+    x, w = randn(g, M, K, dtype=DT[io]), randn(g, N, K, dtype=DT[io], scale=K ** -0.5)
+    b, r = randn(g, N), randn(g, M, N, dtype=DT[io])
+    whole = erd.ssd_linear(x, w, b, "gelu", r)
+    for lo, hi in ((0, 500), (N // 2, N // 2 + 70), (N - 333, N)):
+        part = erd.ssd_linear(x, w[lo:hi].contiguous(), b[lo:hi].contiguous(), "gelu",
+                              r[:, lo:hi].contiguous())
+        assert same_bits(part, whole[:, lo:hi].contiguous()), (lo, hi)
+
+
+@pytest.mark.parametrize("io,K", [("bf16", 1000), ("f32", 520)])
+def test_in_proj_in_two_launches(io, K):
+    sh = erd.Shape(64, 1, 64, 128, 64, io, "f32")
+    g, M, a, cd = gen(K), 200, 64 * 64, 64 * 64 + 256
+    x, w = randn(g, M, K, dtype=DT[io]), randn(g, a + cd + 64, K, dtype=DT[io])
+    z, xBC, d = erd.ssd_in_proj(sh, x, w)
+    for part, lo, hi in ((z.view(M, a), 0, a), (xBC, a, a + cd), (d, a + cd, a + cd + 64)):
+        one = erd.ssd_linear(x, w[lo:hi].contiguous(), out_dtype=part.dtype)
+        assert same_bits(part, one)
+
+
 @pytest.mark.parametrize("M,N,K", SIZES)
 @pytest.mark.parametrize("io", ["bf16", "f32"])
 @pytest.mark.parametrize("act", ["none", "silu", "gelu", "relu2"])
