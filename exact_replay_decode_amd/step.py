@@ -21,6 +21,7 @@ from .api import ReplayCache, Shape, _need, conv_dim
 
 _CODE = {torch.float32: _lib.SSD_F32, torch.bfloat16: _lib.SSD_BF16}
 _raw_stream = torch._C._cuda_getCurrentRawStream
+_new = torch.empty_strided   # (1.2 us where torch.empty takes 1.6)
 
 
 @contextlib.contextmanager
@@ -101,7 +102,7 @@ def ssd_linear(x, weight, bias=None, activation="none", residual=None, out=None,
         out_dtype = x.dtype if out is None else out.dtype
     if out_dtype not in _CODE:
         raise ValueError(f"out_dtype {out_dtype} is not bfloat16 or float32")
-    out = torch.empty((M, N), dtype=out_dtype, device=dev) if out is None else \
+    out = _new((M, N), (N, 1), dtype=out_dtype, device=dev) if out is None else \
         _chk(out, "out", (M, N), out_dtype, dev)
     rc = _lib.load().ssd_linear(M, N, K, io, _CODE[out_dtype], _lib.ACTIVATIONS[activation],
                                 x.data_ptr(), weight.data_ptr(), _p(bias), _p(residual),
@@ -130,9 +131,9 @@ def ssd_in_proj(shape: Shape, u, weight, bias=None, out=None, stream=None):
     if bias is not None:
         _chk(bias, "bias", (N,), torch.float32, dev)
     if out is None:
-        z = torch.empty((M, H, P), dtype=io, device=dev)
-        xBC = torch.empty((M, cd), dtype=io, device=dev)
-        dt = torch.empty((M, H), dtype=dtt, device=dev)
+        z = _new((M, H, P), (H * P, P, 1), dtype=io, device=dev)
+        xBC = _new((M, cd), (cd, 1), dtype=io, device=dev)
+        dt = _new((M, H), (H, 1), dtype=dtt, device=dev)
     else:
         z, xBC, dt = out
         _chk(z, "z", (M, H, P), io, dev)
@@ -160,7 +161,7 @@ def ssd_gated_norm(shape: Shape, y, weight, z=None, groups=None, eps=1e-5,
     _chk(weight, "weight", (shape.H * shape.P,), torch.float32, dev)
     if z is not None:
         _chk(z, "z", full, io, dev)
-    out = torch.empty(full, dtype=io, device=dev) if out is None else \
+    out = torch.empty_like(y) if out is None else \
         _chk(out, "out", full, io, dev)
     rc = _lib.load().ssd_gated_norm(_shape(shape), full[0],
                                     shape.G if groups is None else int(groups), float(eps),
@@ -199,10 +200,10 @@ def ssd_token_logprobs(logits, tokens, top_k=0, out: TokenLogprobs | None = None
     if out is None:
         f, i = torch.float32, torch.int32
         out = TokenLogprobs(
-            torch.empty((T,), dtype=f, device=dev), torch.empty((T,), dtype=f, device=dev),
-            torch.empty((T,), dtype=i, device=dev),
-            torch.empty((T, k), dtype=i, device=dev) if k > 0 else None,
-            torch.empty((T, k), dtype=f, device=dev) if k > 0 else None)
+            _new((T,), (1,), dtype=f, device=dev), _new((T,), (1,), dtype=f, device=dev),
+            _new((T,), (1,), dtype=i, device=dev),
+            _new((T, k), (k, 1), dtype=i, device=dev) if k > 0 else None,
+            _new((T, k), (k, 1), dtype=f, device=dev) if k > 0 else None)
     else:
         _chk(out.logprob, "logprob", (T,), torch.float32, dev)
         if out.entropy is not None:
@@ -253,7 +254,7 @@ def ssd_replay_pages_reserve(shape: Shape, cache: ReplayCache, tokens, slot_idx=
         tok, every = _chk(tokens, "tokens", (n,), torch.int32, dev).data_ptr(), 0
     else:
         tok, every = None, max(0, min(int(tokens), shape.chunk_size))
-    granted = torch.empty((n,), dtype=torch.int32, device=dev) if granted is None else \
+    granted = _new((n,), (1,), dtype=torch.int32, device=dev) if granted is None else \
         _chk(granted, "granted", (n,), torch.int32, dev)
     rc = _lib.load().ssd_replay_pages_reserve(_shape(shape), cs, n, sl, _p(like), tok, every,
                                               granted.data_ptr(), _raw_stream(dev.index))
@@ -320,10 +321,10 @@ def ssd_replay_pages_compact(shape: Shape, cache: ReplayCache, used=None, worksp
             return ssd_replay_pages_compact(shape, cache, used, workspace)
     lib = _lib.load()
     words = lib.ssd_replay_pages_compact_workspace_bytes(cs) // 4
-    used = torch.empty((1,), dtype=torch.int32, device=dev) if used is None else \
+    used = _new((1,), (1,), dtype=torch.int32, device=dev) if used is None else \
         _chk(used, "used", (1,), torch.int32, dev)
     if workspace is None:
-        workspace = torch.empty((words,), dtype=torch.int32, device=dev)
+        workspace = _new((words,), (1,), dtype=torch.int32, device=dev)
     else:
         _chk(workspace, "workspace", (words,), torch.int32, dev)
     rc = lib.ssd_replay_pages_compact(_shape(shape), cs, used.data_ptr(), workspace.data_ptr(),
