@@ -40,19 +40,25 @@ typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
 
 // ---- epilogue ---------------------------------------------------------------
 
-__device__ __forceinline__ float activate(float v, int act) {
-    switch (act) {
-    case SSD_ACT_SILU:
-        return __fdividef(v, 1.0f + __expf(-v));
-    case SSD_ACT_GELU: {
+// v_exp_f32 and v_rcp_f32 are an ulp each; 1 / inf is 0. (One branch for the
+// eight: a switch for each of them and full divisions cost 4 us of 20 in 256 x 128
+// tiles.)
+__device__ __forceinline__ void activate(float (&v)[8], int act) {
+    if (act == SSD_ACT_SILU) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+            v[i] *= __builtin_amdgcn_rcpf(1.0f + __expf(-v[i]));
+    } else if (act == SSD_ACT_GELU) {
         // 0.5 (1 + tanh(u)) = 1 / (1 + exp(-2u)), u = sqrt(2/pi)(v + 0.044715 v^3)
-        const float u2 = 1.5957691216057308f * fmaf(0.044715f * v * v, v, v);
-        return __fdividef(v, 1.0f + __expf(-u2));
-    }
-    case SSD_ACT_RELU2:
-        return v <= 0.0f ? 0.0f : v * v;   // (a NaN stays one)
-    default:
-        return v;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            const float u2 = 1.5957691216057308f * fmaf(0.044715f * v[i] * v[i], v[i], v[i]);
+            v[i] *= __builtin_amdgcn_rcpf(1.0f + __expf(-u2));
+        }
+    } else if (act == SSD_ACT_RELU2) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+            v[i] = v[i] <= 0.0f ? 0.0f : v[i] * v[i];   // (a NaN stays one)
     }
 }
 
@@ -108,10 +114,7 @@ __device__ __forceinline__ void store_eight(const LinearArgs &a, int m, int n, f
                                  : static_cast<const float *>(a.residual)[at + i];
         }
     }
-    if (a.act != SSD_ACT_NONE)
-#pragma unroll
-        for (int i = 0; i < 8; ++i)
-            v[i] = activate(v[i], a.act);
+    activate(v, a.act);
     if (a.residual)
 #pragma unroll
         for (int i = 0; i < 8; ++i)
@@ -252,7 +255,8 @@ struct TileLoader {
             direct_load(lds + lw + 1024 * i, w + kb, ow[i]);
     }
     // The last tile when 2 BK does not divide a row (left: what is there, in units
-    // of 2 bytes): pieces past the row fetch the tile's first piece instead ...
+    // of 2 bytes): pieces past the row fetch the tile's first piece instead, and
+    // count as zeros when they are read.
     __device__ __forceinline__ void load_tail(char *buf, int64_t kb, int left) const {
         const int lane = threadIdx.x & 63, wave = wave_id() - C::L0;
         const uint32_t lds = (uint32_t)(uintptr_t)(lds_void *)buf;
@@ -267,19 +271,6 @@ struct TileLoader {
 #pragma unroll
         for (int i = 0; i < C::LW; ++i)
             direct_load(lds + lw + 1024 * i, w + kb, at(ow[i], wave * C::LW + i));
-    }
-    // ... and, once there, become zeros.
-    __device__ __forceinline__ void zero_tail(char *buf, int left) const {
-        const int lane = threadIdx.x & 63, wave = wave_id() - C::L0;
-        const u32x4 zero = {0, 0, 0, 0};
-#pragma unroll
-        for (int i = 0; i < C::LX; ++i)
-            if (8 * piece(wave * C::LX + i, lane) >= left)
-                *reinterpret_cast<u32x4 *>(buf + lx + 1024 * i + 16 * lane) = zero;
-#pragma unroll
-        for (int i = 0; i < C::LW; ++i)
-            if (8 * piece(wave * C::LW + i, lane) >= left)
-                *reinterpret_cast<u32x4 *>(buf + lw + 1024 * i + 16 * lane) = zero;
     }
 };
 
@@ -301,10 +292,11 @@ __device__ __forceinline__ f32x4 mma_step(const u32x4 &w, const u32x4 &x, f32x4 
 
 // NK steps of an LDS tile, from step k0: the w fragments of a step stay,
 // the x fragments come in groups of two, and the reads of the group after next
-// (and of its step's w) go out before this group's MFMAs.
-template <class C, int NK>
+// (and of its step's w) go out before this group's MFMAs. In the last, partial
+// tile (TAIL) pieces from `left` on are zeros.
+template <class C, int NK, bool TAIL = false>
 __device__ __forceinline__ void tile_steps(const char *buf, f32x4 (&acc)[C::FM][C::FN],
-                                           int k0 = 0) {
+                                           int k0 = 0, int left = 0) {
     constexpr int G = C::FM < 2 ? 1 : 2, NG = C::FM / G;
     constexpr int AHEAD = 2;   // groups read ahead
     constexpr int RX = AHEAD + 1, RW = 1 + (AHEAD + NG - 1) / NG;
@@ -314,17 +306,21 @@ __device__ __forceinline__ void tile_steps(const char *buf, f32x4 (&acc)[C::FM][
     const char *pw = buf + C::XBYTES + ((wave / C::NWM) * C::WN + r) * (2 * C::BK);
     const auto piece = [&](int kk) { return 16 * ((4 * (k0 + kk) + (lane >> 4)) ^ swizzle<C>(r)); };
     u32x4 x[RX][G], w[RW][C::FN];
+    const auto fragment = [&](const char *p, int kk) {
+        u32x4 f = *reinterpret_cast<const u32x4 *>(p + piece(kk));
+        if (TAIL && 8 * (4 * (k0 + kk) + (lane >> 4)) >= left)
+            f = (u32x4){0, 0, 0, 0};
+        return f;
+    };
     const auto read = [&](int s) {
         const int kk = s / NG, g = s % NG;
         if (g == 0)
 #pragma unroll
             for (int j = 0; j < C::FN; ++j)
-                w[kk % RW][j] = *reinterpret_cast<const u32x4 *>(pw + piece(kk) +
-                                                                  j * 16 * (2 * C::BK));
+                w[kk % RW][j] = fragment(pw + j * 16 * (2 * C::BK), kk);
 #pragma unroll
         for (int i = 0; i < G; ++i)
-            x[s % RX][i] = *reinterpret_cast<const u32x4 *>(px + piece(kk) +
-                                                             (g * G + i) * 16 * (2 * C::BK));
+            x[s % RX][i] = fragment(px + (g * G + i) * 16 * (2 * C::BK), kk);
     };
 #pragma unroll
     for (int s = 0; s < AHEAD && s < NK * NG; ++s)
@@ -406,13 +402,10 @@ __global__ __launch_bounds__(64 * C::WAVES) void k_linear_tile(LinearArgs a, int
     }
     if (left) {
         loads_barrier<0>();
-        if (loads)
-            ld.zero_tail(buf + slot * C::BYTES, left);
-        __syncthreads();
         if (works)
 #pragma unroll 1
             for (int k = 0; k < left; k += 32)
-                tile_steps<C, 1>(buf + slot * C::BYTES, acc, k / 32);
+                tile_steps<C, 1, true>(buf + slot * C::BYTES, acc, k / 32, left);
     }
     __syncthreads();
     if (!works)
@@ -456,11 +449,11 @@ __global__ __launch_bounds__(64 * C::WAVES) void k_linear_tile(LinearArgs a, int
 // All shapes give the same bits; the choice is for time alone. A shape's time
 // is modelled as that of its rounds of tiles over the 256 compute units. A
 // round takes fix (us) + K ns with as many workgroups on each compute unit as
-// fit, fix1 and ns1 with one; in between by the line through the two. The bf16
-// figures are fitted to 466 sizes (1 to 8192 rows, 256 to 50280 columns, K 256 to
-// 4096) with weights that come from memory, as a model's do: the shape they pick
-// is 1.8 % slower than the best one in the mean. The fp32 ones are from full
-// rounds at K = 512 and 2048 (1 % on 319 such sizes).
+// fit; a single round that is not full fix1 and ns1 with one on each, in between by
+// the line through the two. (tiles > 0.) The figures are fitted to 466 sizes in
+// bf16 (1 to 8192 rows, 256 to 50280 columns, K 256 to 4096) and 400 in fp32 (half
+// the K), with weights that come from memory, as a model's do: the shape that they
+// pick is 2 % slower than the best one in the mean.
 struct Shape {
     int bm, bn;
     int fit;                 // workgroups that run on a compute unit at a time
@@ -472,13 +465,11 @@ inline float shape_time(const Shape &s, int64_t M, int64_t N, int64_t K) {
     const int64_t tiles = ((M + s.bm - 1) / s.bm) * ((N + s.bn - 1) / s.bn);
     if (tiles > kLinearMaxTiles)
         return INFINITY;
-    const int64_t rounds = tiles / (kUnits * s.fit), rest = tiles - rounds * kUnits * s.fit;
+    const int64_t round = kUnits * s.fit;
     const float one = s.fix1 + (float)K * s.ns1 * 1e-3f, full = s.fix + (float)K * s.ns * 1e-3f;
-    float t = (float)rounds * full;
-    if (rest > 0)
-        t += s.fit == 1 ? one
-                        : one + (full - one) * (float)((rest - 1) / kUnits) / (float)(s.fit - 1);
-    return t;
+    if (tiles > round)
+        return (float)((tiles + round - 1) / round) * full;
+    return s.fit == 1 ? one : one + (full - one) * (float)((tiles - 1) / kUnits) / (float)(s.fit - 1);
 }
 
 template <int S>
@@ -541,12 +532,12 @@ hipError_t launch_tile(const LinearArgs &a, hipStream_t stream) {
 
 hipError_t linear_bf16(const LinearArgs &args, hipStream_t stream) {
     static constexpr Shape kShapes[] = {
-        {16, 16, 3, 0.10f, 1.39f, 0.53f, 3.19f},    {16, 16, 2, 0.27f, 1.09f, 1.44f, 2.91f},
-        {16, 32, 2, 0.24f, 1.56f, 1.38f, 4.42f},    {64, 32, 1, 0.75f, 2.59f, 0.75f, 2.59f},
-        {64, 64, 2, 0.56f, 5.15f, 1.28f, 8.09f},    {64, 64, 1, 1.15f, 4.37f, 1.15f, 4.37f},
-        {128, 64, 2, 0.64f, 6.75f, 2.03f, 10.78f},  {128, 64, 1, 1.84f, 5.75f, 1.84f, 5.75f},
-        {128, 128, 1, 3.01f, 8.75f, 3.01f, 8.75f},  {256, 128, 1, 5.97f, 12.41f, 5.97f, 12.41f},
-        {256, 256, 1, 9.99f, 23.53f, 9.99f, 23.53f},
+        {16, 16, 3, 0.09f, 1.39f, 0.43f, 3.09f},    {16, 16, 2, 0.27f, 1.09f, 1.37f, 2.67f},
+        {16, 32, 2, 0.24f, 1.55f, 1.30f, 4.05f},    {64, 32, 1, 0.60f, 2.42f, 1.19f, 2.67f},
+        {64, 64, 2, 0.54f, 5.19f, 1.27f, 7.68f},    {64, 64, 1, 0.92f, 4.08f, 1.65f, 4.72f},
+        {128, 64, 2, 0.61f, 6.79f, 1.92f, 10.38f},  {128, 64, 1, 1.48f, 5.59f, 2.34f, 5.85f},
+        {128, 128, 1, 2.31f, 8.40f, 3.53f, 9.20f},  {256, 128, 1, 4.72f, 11.52f, 6.41f, 12.78f},
+        {256, 256, 1, 8.50f, 23.79f, 10.43f, 23.49f},
     };
     return by_columns(kShapes, args, [&](int shape, const LinearArgs &a) {
         switch (shape) {
@@ -566,23 +557,26 @@ hipError_t linear_bf16(const LinearArgs &args, hipStream_t stream) {
 }
 
 // fp32 is bound by the matrix instructions from 32 x 32 on (131 of 157 TFLOP/s
-// peak in full rounds): the shapes differ in how evenly the tiles divide.
+// peak in full rounds of 128 x 128): the shapes differ in how evenly the tiles divide.
 hipError_t linear_f32(const LinearArgs &args, hipStream_t stream) {
     static constexpr Shape kShapes[] = {
-        {16, 16, 3, 0.0f, 5.8f, 0.4f, 7.3f},     {16, 16, 1, 0.2f, 5.35f, 0.2f, 5.35f},
-        {32, 32, 2, 0.3f, 5.8f, 1.5f, 8.75f},    {64, 32, 3, 0.3f, 11.5f, 2.0f, 23.6f},
-        {64, 32, 1, 0.9f, 9.4f, 0.9f, 9.4f},     {64, 64, 2, 1.2f, 19.2f, 2.9f, 29.5f},
-        {128, 64, 3, 2.5f, 33.2f, 5.7f, 85.0f},  {128, 128, 2, 5.4f, 62.0f, 7.8f, 112.6f},
+        {16, 16, 3, 0.00f, 4.46f, 0.57f, 5.97f},    {32, 32, 2, 0.00f, 4.95f, 2.29f, 7.69f},
+        {32, 32, 3, 0.00f, 6.46f, 1.57f, 11.64f},   {32, 64, 3, 0.00f, 11.44f, 2.36f, 20.28f},
+        {64, 32, 3, 0.00f, 10.78f, 2.25f, 21.16f},  {64, 32, 1, 0.00f, 8.73f, 1.89f, 8.84f},
+        {64, 64, 2, 0.00f, 20.37f, 2.00f, 30.86f},  {96, 64, 2, 0.06f, 26.22f, 2.13f, 43.62f},
+        {128, 64, 3, 0.82f, 35.11f, 5.34f, 77.40f}, {128, 128, 2, 2.31f, 64.76f, 5.29f, 113.08f},
     };
     return by_columns(kShapes, args, [&](int shape, const LinearArgs &a) {
         switch (shape) {
         case 0: return launch_tile<Tile<true, 16, 16, 16, 16, 256, 3, 4>>(a, stream);
-        case 1: return launch_tile<Tile<true, 16, 16, 16, 16, 512, 5, 8>>(a, stream);
-        case 2: return launch_tile<Tile<true, 32, 32, 16, 16, 256, 2, 8, true>>(a, stream);
-        case 3: return launch_tile<Tile<true, 64, 32, 32, 16, 128, 2>>(a, stream);
-        case 4: return launch_tile<Tile<true, 64, 32, 32, 16, 256, 3, 4, true>>(a, stream);
-        case 5: return launch_tile<Tile<true, 64, 64, 32, 32, 128, 2>>(a, stream);
-        case 6: return launch_tile<Tile<true, 128, 64, 32, 32, 64, 2>>(a, stream);
+        case 1: return launch_tile<Tile<true, 32, 32, 16, 16, 256, 2, 8, true>>(a, stream);
+        case 2: return launch_tile<Tile<true, 32, 32, 16, 16, 128, 3>>(a, stream);
+        case 3: return launch_tile<Tile<true, 32, 64, 16, 16, 128, 2>>(a, stream);
+        case 4: return launch_tile<Tile<true, 64, 32, 32, 16, 128, 2>>(a, stream);
+        case 5: return launch_tile<Tile<true, 64, 32, 32, 16, 256, 3, 4, true>>(a, stream);
+        case 6: return launch_tile<Tile<true, 64, 64, 32, 32, 128, 2>>(a, stream);
+        case 7: return launch_tile<Tile<true, 96, 64, 32, 16, 128, 2, 4>>(a, stream);
+        case 8: return launch_tile<Tile<true, 128, 64, 32, 32, 64, 2>>(a, stream);
         default: return launch_tile<Tile<true, 128, 128, 32, 64, 64, 2>>(a, stream);
         }
     });

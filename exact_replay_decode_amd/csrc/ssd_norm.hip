@@ -72,9 +72,11 @@ struct Eight<IoF32> {
     }
 };
 
-// SiLU with the hardware exp2 and reciprocal (a few ulps, far below the bf16
-// rounding), as in the conv before the scan.
-__device__ __forceinline__ float silu(float z) { return __fdividef(z, 1.0f + __expf(-z)); }
+// SiLU with the hardware exp2 and reciprocal (an ulp each, far below the bf16
+// rounding; 1 / inf is 0).
+__device__ __forceinline__ float silu(float z) {
+    return z * __builtin_amdgcn_rcpf(1.0f + __expf(-z));
+}
 
 // The lane's pieces of one group, lanes apart: the gated values and their sum of
 // squares, then the scaled output.

@@ -38,7 +38,15 @@ TILES = [(1, 17, 1000), (1, 4100, 40), (1, 4100, 136), (33, 4100, 40), (33, 4100
          (65, 4100, 4104), (200, 8200, 1000), (65, 33000, 520), (129, 33000, 264),
          (400, 33000, 264), (700, 16001, 520), (2049, 4100, 520), (2049, 10300, 520),
          (4097, 1000, 520), (200, 33000, 40), (700, 8200, 40), (4097, 2000, 40),
-         (513, 33000, 136)]
+         (513, 33000, 136), (4097, 17, 40), (33, 8200, 264), (129, 8200, 40), (100, 8200, 40),
+         (65, 8200, 4104), (100, 8200, 2056), (129, 10300, 1000), (300, 10300, 520),
+         (33, 33000, 264), (65, 33000, 136), (700, 8200, 136), (1025, 6001, 136),
+         (200, 10300, 1000), (513, 8200, 264), (4097, 2000, 136), (2049, 8200, 40),
+         (33, 33000, 40), (65, 33000, 40), (300, 33000, 40), (400, 33000, 72), (2049, 4100, 136),
+         (2049, 4100, 1000), (513, 16001, 520), (2049, 10300, 264), (4097, 6001, 520),
+         (4097, 1000, 136), (2049, 1000, 520), (400, 10300, 136), (4097, 4100, 40),
+         (4097, 1000, 40), (4097, 10300, 40), (33, 16001, 264), (1, 16001, 520),
+         (257, 16001, 136), (200, 8200, 264)]
 
 
 @pytest.mark.parametrize("M,N,K", TILES)
