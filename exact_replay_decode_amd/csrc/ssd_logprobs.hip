@@ -9,7 +9,7 @@
 // the stream's chunks in order, then a DPP tree over the wave, then the 16
 // streams in order. So the sums' order depends on V alone, and a row's bits
 // depend neither on the number of rows nor on how many waves share the row
-// (4, or 16 when there are few rows).
+// (4 or 16).
 //
 // The best top_k in short steps after the pass, from what the softmax needs
 // anyway, the maxima of each lane's 32 elements of a chunk (a segment; kept in
@@ -249,8 +249,10 @@ struct Segs {
     static constexpr int ORD = 64 / NW;
 };
 
+// (bf16: 64 registers, so that two workgroups of 16 waves share a compute unit)
 template <class IO, int NW, bool TOP>
-__global__ __launch_bounds__(64 * NW) void k_logprobs(LogprobArgs a) {
+__global__ __launch_bounds__(64 * NW, NW == 16 && sizeof(typename IO::T) == 2 ? 8 : 1)
+void k_logprobs(LogprobArgs a) {
     using T = typename IO::T;
     constexpr int E = Chunk<IO>::E, NV = Regs<IO>::NV, ORD = Segs<NW>::ORD;
     constexpr int LIST = NW == 4 ? 256 : 128;
@@ -560,10 +562,16 @@ __global__ __launch_bounds__(64 * NW) void k_logprobs(LogprobArgs a) {
     }
 }
 
+// 16 waves a row while all rows run at the same time (bf16 two to a compute unit: 512
+// rows of 50280 in 21 against 32 us, 1024 rows in 40 against 44, 2048 in 77 against 77
+// with top 8, in 56 against 46 without; fp32 one: 256 rows in 12 against 16 us, 512 in
+// 24 against 22), and in bf16 where every wave has four chunks or more (2048 rows of
+// 131072 with top 8: 146 against 176 us).
 template <class IO>
 hipError_t logprobs_impl(const LogprobArgs &a, hipStream_t stream) {
+    constexpr bool BF = sizeof(typename IO::T) == 2;
     const dim3 grid((unsigned)a.T);
-    if (a.T <= 256) {
+    if (a.T <= (BF ? 512 : 256) || (BF && a.V >= 4 * kStreams * kChunkElems)) {
         if (a.k > 0)
             k_logprobs<IO, 16, true><<<grid, dim3(1024), 0, stream>>>(a);
         else

@@ -85,7 +85,7 @@ def test_matches_fp64(V, io):
 
 
 @pytest.mark.parametrize("io", ["bf16", "f32"])
-@pytest.mark.parametrize("T", [4, 300])
+@pytest.mark.parametrize("T", [4, 300, 600])
 def test_ties_masks_and_orders(io, T):
     """Equal values (index decides), rows in ascending and descending order,
     masks that leave few, one or no token, whole chunks masked."""
@@ -162,7 +162,7 @@ def test_tokens_out_of_range():
 
 
 @pytest.mark.parametrize("io", ["bf16", "f32"])
-@pytest.mark.parametrize("V", [777, 50257])
+@pytest.mark.parametrize("V", [777, 50257, 131073])
 def test_rows_do_not_depend_on_the_call(io, V):
     g = gen(V)
     x = randn(g, 700, V, dtype=DT[io], scale=2.0)
