@@ -25,7 +25,9 @@
 // rank counts the elements ahead of the token with one comparison each.
 //
 // Measured: 4096 rows of 50280 bf16 in 89 us without alternatives (4.6 TB/s), where
-// the vector unit's work (a row's elements at 48 cycles per 64) is 63 us.
+// the vector unit's work (a row's elements at 48 cycles per 64) is 63 us; an operation
+// an element fewer changed nothing, so the waits between chunks bound it. 512 rows of
+// 131072 with one token in 500 allowed and top 8: 30-32 us, 4.2-4.5 TB/s.
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 

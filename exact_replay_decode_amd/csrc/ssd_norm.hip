@@ -11,7 +11,8 @@
 // fixed order: a lane's values in turn, a tree over the lanes, the waves' sums in
 // order. The order depends on gs alone, so a row's bits do not depend on the
 // number of rows.
-// It is a stream: 16384 rows of 64 heads in 8 groups (403 MB) take 71-76 us, 5.3-5.7 TB/s.
+// It is a stream: 16384 rows of 64 heads in 8 groups (403 MB) take 70-75 us, 5.4-5.8
+// TB/s (a copy of 1 GiB moves 5.0).
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
