@@ -237,3 +237,16 @@ def test_other_stream():
     y = erd.ssd_linear(x, w, stream=s)
     s.synchronize()
     assert same_bits(y, want)
+
+
+@pytest.mark.parametrize("M,N,K", [(140000, 24, 16384), (70000, 65544, 8)])
+def test_rows_past_32_bits(M, N, K):
+    """x of more than 2**31 elements, and an output of more than 2**32."""
+    g = gen(K)
+    x = torch.empty(M, K, dtype=torch.bfloat16, device=DEV)
+    for a in range(0, M, 20000):
+        x[a:a + 20000] = randn(g, *x[a:a + 20000].shape)
+    w = randn(g, N, K, dtype=torch.bfloat16)
+    y = erd.ssd_linear(x, w, activation="relu2")
+    for a in (0, M // 2, M - 3):
+        assert same_bits(y[a:a + 3], erd.ssd_linear(x[a:a + 3], w, activation="relu2"))

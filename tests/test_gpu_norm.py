@@ -95,3 +95,16 @@ def test_refusals_and_empty():
         erd.ssd_gated_norm(sh, y, w[:32])
     with pytest.raises(ValueError, match="dtype"):
         erd.ssd_gated_norm(sh, y, w, z=y.float())
+
+
+def test_rows_past_32_bits():
+    """More than 2**31 elements in each array."""
+    sh = erd.Shape(64, 8, 64, 16, 64)
+    T, g = 530000, gen(6)
+    y = torch.empty(T, 64, 64, dtype=torch.bfloat16, device=DEV)
+    for a in range(0, T, 53000):
+        y[a:a + 53000] = randn(g, 53000, 64, 64)
+    z, w = y.flip(0), randn(g, 4096)
+    whole = erd.ssd_gated_norm(sh, y, w, z=z)
+    for a in (0, T // 2, T - 2):
+        assert same_bits(erd.ssd_gated_norm(sh, y[a:a + 2], w, z=z[a:a + 2]), whole[a:a + 2])

@@ -210,6 +210,32 @@ def test_one_table_for_the_caches_of_two_layers():
                 assert p != q and same_bits(rows[p], rows[q])
 
 
+def test_pages_that_two_slots_share():
+    """A page that two table entries name is used once, is not handed out, and
+    both entries follow it when the pool is compacted."""
+    sh, c = _cache(6)
+    c.buf_pages[2, :2] = c.buf_pages[4, :2]        # slot 2 reads slot 4's first pages
+    rows = c.buf_x.view(-1, *c.buf_x.shape[-2:])
+    pages = c.buf_pages.cpu()
+    held = {int(p) for p in pages.flatten() if p >= 0}
+    want = [rows[int(p) * 16:int(p) * 16 + 16].clone() if p >= 0 else None
+            for p in pages.flatten()]
+    used = erd.ssd_replay_pages_compact(sh, c)
+    assert int(used) == len(held) and int(c.buf_pages.max()) == len(held) - 1
+    assert same_bits(c.buf_pages[2, :2], c.buf_pages[4, :2])
+    for p, w in zip(c.buf_pages.cpu().flatten().tolist(), want):
+        assert (p < 0) == (w is None)
+        if w is not None:
+            assert same_bits(rows[p * 16:p * 16 + 16], w)
+    free = 40 - len(held)
+    i32 = dict(dtype=torch.int32, device=DEV)
+    got = erd.ssd_replay_pages_reserve(sh, c, 64, slot_idx=torch.tensor([0, 1, 3], **i32))
+    lack = [4 - 2, 4 - 1, 4 - 3]
+    assert sum(lack) <= free and bool(got.all())
+    new = sorted(set(c.buf_pages.flatten().tolist()) - {-1})
+    assert new == list(range(len(held) + sum(lack)))
+
+
 def test_lists_with_skipped_and_empty_entries():
     """An empty list does nothing; entries out of range are skipped in every
     call, and the rest is served."""
