@@ -9,11 +9,12 @@
 // keeps the answer a pure function of the table (lowest page first), with no
 // free list that could disagree with it, and a table of 8192 entries is
 // 32 KB, read once.
-// That plan is latency, not bytes: 512 slots of 16 pages take 8.8 us (the table's
-// one round trip, the bits, two prefix sums, the search).
+// That plan is latency, not bytes: 512 slots of 16 pages take 5.9 us (the table's
+// one round trip beside the requests', the bits, two prefix sums, the search); with the
+// requests' rows read an entry at a time, and before the table, 8.7.
 // The copies move whole 16-byte pieces, eight loads in flight per thread
 // before the first store: 16 slots forked into 128 (272 MB written, 34 MB read) in
-// 53-57 us, 5.4-5.8 TB/s, where a fill of that size takes 40; 71 MB of pages moved in
+// 53-59 us, 5.2-5.8 TB/s, where a fill of that size takes 40; 71 MB of pages moved in
 // 23-25 us, 5.6-6.2 TB/s of both directions.
 #include <hip/hip_runtime.h>
 #include <stdint.h>
@@ -208,24 +209,20 @@ __global__ __launch_bounds__(256) void k_pages_trim(SlotMap c, int n, const int3
 
 // ---- planning ---------------------------------------------------------------
 
-// Exclusive prefix sum over the workgroup of kPlan threads; *total gets the
-// sum. red: 16 ints of LDS, free on entry and on return.
+// Exclusive prefix sum over the workgroup of kPlan threads, of counts whose total is
+// below 2^24 (exact in fp32, for the DPP scan); *total gets the sum. red: 16 ints of
+// LDS, free on entry and on return.
 __device__ __forceinline__ int block_exclusive(int v, int *red, int *total) {
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-    int x = v;
-    for (int o = 1; o < 64; o <<= 1) {
-        const int y = __shfl_up(x, o, 64);
-        if (lane >= o)
-            x += y;
-    }
+    const int x = (int)wave_scan_inclusive((float)v);
     if (lane == 63)
         red[wave] = x;
     __syncthreads();
     int before = 0, all = 0;
+#pragma unroll
     for (int w = 0; w < kPlan / 64; ++w) {
         const int t = red[w];
-        if (w < wave)
-            before += t;
+        before += w < wave ? t : 0;
         all += t;
     }
     __syncthreads();
@@ -269,7 +266,21 @@ struct PageBits {
     uint32_t *bits;       // [words], a set bit is a used page
     int32_t *first;       // [kPlan]: free pages below thread t's words
     int words, per, num_pages, nfree;
+    int head[8];          // the thread's first eight table entries
 
+    // table entries i0, i0 + kPlan, ..; -1 past the end
+    __device__ static __forceinline__ void load(const SlotMap &c, int64_t i0, int (&p)[8]) {
+        const int64_t n = (int64_t)c.num_slots * c.npp;
+#pragma unroll
+        for (int k = 0; k < 8; ++k)
+            p[k] = i0 + k * kPlan < n ? c.pages[i0 + k * kPlan] : -1;
+    }
+    __device__ __forceinline__ void mark(const SlotMap &c, const int (&p)[8]) {
+#pragma unroll
+        for (int k = 0; k < 8; ++k)
+            if (page_ok(c, p[k]))
+                atomicOr(&bits[p[k] >> 5], 1u << (p[k] & 31));
+    }
     // pages that exist in word w
     __device__ uint32_t valid(int w) const {
         const int left = num_pages - w * 32;
@@ -279,21 +290,18 @@ struct PageBits {
         : bits(bits_), first(first_), num_pages(c.num_pages) {
         words = (num_pages + 31) / 32;
         per = (words + kPlan - 1) / kPlan;
+        // (eight entries a thread in flight, the first eight while the bits are
+        // cleared: the table's latency, not its size, is what this costs)
+        load(c, threadIdx.x, head);
         for (int w = threadIdx.x; w < words; w += kPlan)
             bits[w] = 0;
         __syncthreads();
-        // (eight entries a thread in flight: the table's latency, not its size,
-        // is what this costs)
+        mark(c, head);
         const int64_t n = (int64_t)c.num_slots * c.npp;
-        for (int64_t i0 = threadIdx.x; i0 < n; i0 += 8 * kPlan) {
+        for (int64_t i0 = threadIdx.x + 8 * kPlan; i0 < n; i0 += 8 * kPlan) {
             int p[8];
-#pragma unroll
-            for (int k = 0; k < 8; ++k)
-                p[k] = i0 + k * kPlan < n ? c.pages[i0 + k * kPlan] : -1;
-#pragma unroll
-            for (int k = 0; k < 8; ++k)
-                if (page_ok(c, p[k]))
-                    atomicOr(&bits[p[k] >> 5], 1u << (p[k] & 31));
+            load(c, i0, p);
+            mark(c, p);
         }
         __syncthreads();
         const int w0 = threadIdx.x * per, w1 = min(w0 + per, words);
@@ -309,11 +317,16 @@ struct PageBits {
     }
 };
 
-// A request: its slot (-1: skipped), the pages its tokens span and the ones it
-// lacks, as a bit mask (a slot has at most kMaxQ / 16 = 16 pages).
+// A request: its slot (-1: skipped), and its table row, its length and its tokens as
+// loaded. (A slot has 1, 2, 4, 8 or 16 pages; the row is fetched in 16-byte pieces,
+// since 64 lanes read 64 rows.)
 struct Request {
-    int slot, lack;
-    __device__ __forceinline__ Request(const ReserveArgs &a, int b) : slot(-1), lack(0) {
+    int slot, len, tok;
+    typedef int i32x4 __attribute__((ext_vector_type(4)));
+    i32x4 e[kMaxQ / 64];
+    __device__ __forceinline__ Request(const ReserveArgs &a, int b)
+        : slot(-1), len(0), tok(0), e{} {
+        typedef i32x4 i32x4_u __attribute__((aligned(4)));
         const SlotMap &c = a.c;
         if (b >= a.n)
             return;
@@ -322,21 +335,32 @@ struct Request {
         if (s < 0 || s >= c.num_slots || like < 0 || like >= c.num_slots)
             return;
         const int32_t *row = c.pages + (int64_t)s * c.npp;
-        int e[kMaxQ / 16];
+        if (c.npp >= 4) {
 #pragma unroll
-        for (int i = 0; i < kMaxQ / 16; ++i)
-            e[i] = i < c.npp ? row[i] : 0;
-        const int len = c.buf_len[like];
-        int tok = a.tokens ? a.tokens[b] : a.tokens_all;
-        tok = tok < 0 ? 0 : (tok > c.Q ? c.Q : tok);
-        if (len < 0 || len >= c.Q)
-            return;
+            for (int i = 0; i < kMaxQ / 64; ++i)
+                e[i] = *reinterpret_cast<const i32x4_u *>(row + (4 * i < c.npp ? 4 * i : 0));
+        } else {
+            e[0] = (i32x4){row[0], row[c.npp - 1], -1, -1};
+        }
         slot = s;
-        const int pages = (min(len + tok, c.Q) + (1 << c.shift) - 1) >> c.shift;
+        len = c.buf_len[like];
+        tok = a.tokens ? a.tokens[b] : a.tokens_all;
+    }
+    // The pages that its tokens span and that it lacks, as a bit mask; a slot that
+    // cannot be served becomes -1.
+    __device__ __forceinline__ int lack(const SlotMap &c) {
+        if (slot < 0 || len < 0 || len >= c.Q) {
+            slot = -1;
+            return 0;
+        }
+        const int t = min(max(tok, 0), c.Q);
+        const int pages = (min(len + t, c.Q) + (1 << c.shift) - 1) >> c.shift;
+        int m = 0;
 #pragma unroll
         for (int i = 0; i < kMaxQ / 16; ++i)
-            if (i < pages && !page_ok(c, e[i]))
-                lack |= 1 << i;
+            if (i < pages && !page_ok(c, e[i / 4][i % 4]))
+                m |= 1 << i;
+        return m;
     }
 };
 
@@ -353,14 +377,15 @@ __global__ __launch_bounds__(kPlan) void k_pages_reserve(ReserveArgs a) {
         const int b = b0 + threadIdx.x;
         if (b0 > 0)
             q = Request(a, b);
-        const int need = __popc(q.lack);
+        const int lack = q.lack(c);
+        const int need = __popc(lack);
         int total;
         int r = asked + block_exclusive(need, red, &total);
         asked += total;
         const bool served = q.slot >= 0 && (need == 0 || r + need <= pb.nfree);
         if (served) {
             int32_t *row = c.pages + (int64_t)q.slot * c.npp;
-            for (int m = q.lack; m; m &= m - 1)
+            for (int m = lack; m; m &= m - 1)
                 row[__ffs(m) - 1] = pb.free_page(r++);
         }
         if (b < a.n && a.granted)
@@ -395,11 +420,13 @@ __global__ __launch_bounds__(kPlan) void k_compact_plan(SlotMap c, int32_t *used
         work[3 + 2 * j] = pb.free_page(j);
     }
     const int64_t n = (int64_t)c.num_slots * c.npp;
+    int e[8];
     for (int64_t i0 = threadIdx.x; i0 < n; i0 += 8 * kPlan) {
-        int e[8];
 #pragma unroll
         for (int k = 0; k < 8; ++k)
-            e[k] = i0 + k * kPlan < n ? c.pages[i0 + k * kPlan] : -1;
+            e[k] = pb.head[k];
+        if (i0 >= 8 * kPlan)
+            PageBits::load(c, i0, e);
 #pragma unroll
         for (int k = 0; k < 8; ++k) {
             const int p = e[k];
