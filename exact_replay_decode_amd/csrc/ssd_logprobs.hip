@@ -24,7 +24,7 @@
 // are then joined.
 // rank counts the elements ahead of the token with one comparison each.
 //
-// Measured: 4096 rows of 50280 bf16 in 89 us without alternatives (4.6 TB/s), where
+// Measured: 4096 rows of 50280 bf16 in 84 us without alternatives (4.9 TB/s), where
 // the vector unit's work (a row's elements at 48 cycles per 64) is 63 us; an operation
 // an element fewer changed nothing, so the waits between chunks bound it. 512 rows of
 // 131072 with one token in 500 allowed and top 8: 30-32 us, 4.2-4.5 TB/s.
@@ -251,16 +251,17 @@ struct Segs {
     static constexpr int ORD = 64 / NW;
 };
 
-// (bf16: 64 registers, so that two workgroups of 16 waves share a compute unit)
+// (bf16: 64 registers and less than 20 KB of LDS, so that 32 waves share a compute unit:
+// 2048 rows of 50280 with top 8 in 52 us, 60 with 28 waves)
 template <class IO, int NW, bool TOP>
-__global__ __launch_bounds__(64 * NW, NW == 16 && sizeof(typename IO::T) == 2 ? 8 : 1)
+__global__ __launch_bounds__(64 * NW, sizeof(typename IO::T) == 2 ? 8 : 1)
 void k_logprobs(LogprobArgs a) {
     using T = typename IO::T;
     constexpr int E = Chunk<IO>::E, NV = Regs<IO>::NV, ORD = Segs<NW>::ORD;
     constexpr int LIST = NW == 4 ? 256 : 128;
     // segment maxima; past the listing of the segments the candidates, or the lists
     __shared__ __attribute__((aligned(8))) float smax[TOP ? NW * ORD * 64 : 1];
-    __shared__ uint32_t few[TOP ? kSegs : 1];       // segments
+    __shared__ uint16_t few[TOP ? kSegs : 1];       // segments
     uint64_t *cand = reinterpret_cast<uint64_t *>(smax);
     __shared__ float st[kStreams][3];
     __shared__ int ahead_of[NW], ln[NW];
@@ -380,7 +381,7 @@ void k_logprobs(LogprobArgs a) {
 
     if (TOP && wave == 1) {
         // (64 groups bound a small top_k well enough; the other waves wait here:
-        // 94 against 98 us for 4096 x 50280, top 5)
+        // 4 us of 98 for 4096 x 50280, top 5)
         const float g = gm[2 * lane], h = gm[2 * lane + 1];
         const float tau = a.k <= 24 ? wave_kth(fmaxf(g, h), a.k) : wave_kth(g, h, a.k);
         if (lane == 0)
@@ -446,7 +447,7 @@ void k_logprobs(LogprobArgs a) {
         if (m) {
             const int at = append_at(m, &count[0]);
             if (((m >> lane) & 1) && at < kSegs)
-                few[at] = (uint32_t)((wave * ORD + o) * 64 + lane);
+                few[at] = (uint16_t)((wave * ORD + o) * 64 + lane);
         }
     }
     __syncthreads();
@@ -565,10 +566,9 @@ void k_logprobs(LogprobArgs a) {
 }
 
 // 16 waves a row while all rows run at the same time (bf16 two to a compute unit: 512
-// rows of 50280 in 21 against 32 us, 1024 rows in 40 against 44, 2048 in 77 against 77
-// with top 8, in 56 against 46 without; fp32 one: 256 rows in 12 against 16 us, 512 in
-// 24 against 22), and in bf16 where every wave has four chunks or more (2048 rows of
-// 131072 with top 8: 146 against 176 us).
+// rows of 50280 with top 8 in 18 against 24 us, 1024 in 33 against 33, 2048 in 62 against
+// 52; fp32 one: 256 rows in 14 against 18 us, 512 in 28 against 25), and in bf16 where
+// every wave has four chunks or more (2048 rows of 131072 with top 8: 102 against 108 us).
 template <class IO>
 hipError_t logprobs_impl(const LogprobArgs &a, hipStream_t stream) {
     constexpr bool BF = sizeof(typename IO::T) == 2;
