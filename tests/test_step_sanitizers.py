@@ -7,11 +7,11 @@ import shutil
 
 import pytest
 
-from test_native_sanitizers import CSRC, NATIVE, ROOT, _build_and_run
-
 
 @pytest.mark.skipif(shutil.which("g++") is None, reason="g++ not available")
 def test_step_layer_under_sanitizers(tmp_path):
+    # (imported here: the file may be left out where only the GPU tests run)
+    from test_native_sanitizers import CSRC, NATIVE, ROOT, _build_and_run
     out = _build_and_run(
         tmp_path, "g++",
         [os.path.join(CSRC, "ssd_step_api.cpp"), os.path.join(NATIVE, "step_host_check.cpp")],
