@@ -51,7 +51,8 @@ def random_cache(slots, Q, pt, num_pages, seed, H=3, G=1, P=16, N=16, io="bf16",
 
 
 SIZES = [(1, 16, 16, 1), (3, 64, 16, 12), (7, 64, 16, 33), (40, 256, 16, 700), (40, 256, 64, 100),
-         (300, 256, 16, 4000), (1500, 32, 16, 2600), (2100, 64, 16, 40000)]
+         (50, 128, 16, 300), (70, 256, 32, 400), (300, 256, 16, 4000), (1500, 32, 16, 2600),
+         (2100, 64, 16, 40000)]
 
 
 @pytest.mark.parametrize("slots,Q,pt,num_pages", SIZES)
