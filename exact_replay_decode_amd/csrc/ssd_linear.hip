@@ -451,10 +451,12 @@ __global__ __launch_bounds__(64 * C::WAVES) void k_linear_tile(LinearArgs a, int
 // is modelled as that of its rounds of tiles over the 256 compute units. A
 // round takes fix (us) + K ns with as many workgroups on each compute unit as
 // fit; a single round that is not full fix1 and ns1 with one on each, in between by
-// the line through the two. (tiles > 0.) The figures are fitted to 466 sizes in
-// bf16 (1 to 8192 rows, 256 to 50280 columns, K 256 to 4096) and 400 in fp32 (half
-// the K), with weights that come from memory, as a model's do: the shape that they
-// pick is 2 % slower than the best one in the mean.
+// the line through the two. In bf16 that counts no further down than the time of
+// the arrays at 5.2 TB/s (but a fiftieth of it, for shapes that are all bound by
+// them). The figures are fitted to 466 sizes in bf16 (1 to 8192 rows, 256 to 50280
+// columns, K 256 to 4096) and 400 in fp32 (half the K), with weights that come from
+// memory, as a model's do: the shape that they pick is 1.2 % (fp32 1.8 %) slower than
+// the best one in the mean.
 struct Shape {
     int bm, bn;
     int fit;                 // workgroups that run on a compute unit at a time
@@ -462,23 +464,27 @@ struct Shape {
 };
 constexpr int kUnits = 256;
 
-inline float shape_time(const Shape &s, int64_t M, int64_t N, int64_t K) {
+inline float shape_time(const Shape &s, int64_t M, int64_t N, int64_t K, bool bf16) {
     const int64_t tiles = ((M + s.bm - 1) / s.bm) * ((N + s.bn - 1) / s.bn);
     if (tiles > kLinearMaxTiles)
         return INFINITY;
     const int64_t round = kUnits * s.fit;
     const float one = s.fix1 + (float)K * s.ns1 * 1e-3f, full = s.fix + (float)K * s.ns * 1e-3f;
+    float t = one;
     if (tiles > round)
-        return (float)((tiles + round - 1) / round) * full;
-    return s.fit == 1 ? one : one + (full - one) * (float)((tiles - 1) / kUnits) / (float)(s.fit - 1);
+        t = (float)((tiles + round - 1) / round) * full;
+    else if (s.fit > 1)
+        t += (full - one) * (float)((tiles - 1) / kUnits) / (float)(s.fit - 1);
+    const float bytes = 2.0f * ((float)N * (float)K + (float)M * (float)K + (float)M * (float)N);
+    return bf16 ? std::max(t, bytes / 5.2e6f) + 0.02f * t : t;
 }
 
 template <int S>
-int best_shape(const Shape (&s)[S], int64_t M, int64_t N, int64_t K, float *time) {
+int best_shape(const Shape (&s)[S], int64_t M, int64_t N, int64_t K, bool bf16, float *time) {
     int best = 0;
-    *time = shape_time(s[0], M, N, K);
+    *time = shape_time(s[0], M, N, K, bf16);
     for (int i = 1; i < S; ++i) {
-        const float t = shape_time(s[i], M, N, K);
+        const float t = shape_time(s[i], M, N, K, bf16);
         if (t < *time) {
             *time = t;
             best = i;
@@ -496,15 +502,15 @@ constexpr float kSecondLaunch = 2.0f;
 template <int S, class F>
 hipError_t by_columns(const Shape (&s)[S], LinearArgs a, F each) {
     float best, rest_time;
-    int first = best_shape(s, a.M, a.N, a.K, &best), second = 0;
+    int first = best_shape(s, a.M, a.N, a.K, a.io_bf16, &best), second = 0;
     int64_t n1 = a.N;
     for (int i = 0; i < S; ++i) {
         const int64_t mt = (a.M + s[i].bm - 1) / s[i].bm, nt = (a.N + s[i].bn - 1) / s[i].bn;
         const int64_t round = kUnits * s[i].fit, cols = mt * nt / round * round / mt * s[i].bn;
         if (cols <= 0 || cols >= a.N)
             continue;
-        const int j = best_shape(s, a.M, a.N - cols, a.K, &rest_time);
-        const float t = shape_time(s[i], a.M, cols, a.K) + rest_time + kSecondLaunch;
+        const int j = best_shape(s, a.M, a.N - cols, a.K, a.io_bf16, &rest_time);
+        const float t = shape_time(s[i], a.M, cols, a.K, a.io_bf16) + rest_time + kSecondLaunch;
         if (t < best) {
             best = t;
             first = i;
@@ -533,25 +539,28 @@ hipError_t launch_tile(const LinearArgs &a, hipStream_t stream) {
 
 hipError_t linear_bf16(const LinearArgs &args, hipStream_t stream) {
     static constexpr Shape kShapes[] = {
-        {16, 16, 3, 0.09f, 1.39f, 0.43f, 3.09f},    {16, 16, 2, 0.27f, 1.09f, 1.37f, 2.67f},
-        {16, 32, 2, 0.24f, 1.55f, 1.30f, 4.05f},    {64, 32, 1, 0.60f, 2.42f, 1.19f, 2.67f},
-        {64, 64, 2, 0.54f, 5.19f, 1.27f, 7.68f},    {64, 64, 1, 0.92f, 4.08f, 1.65f, 4.72f},
-        {128, 64, 2, 0.61f, 6.79f, 1.92f, 10.38f},  {128, 64, 1, 1.48f, 5.59f, 2.34f, 5.85f},
-        {128, 128, 1, 2.31f, 8.40f, 3.53f, 9.20f},  {256, 128, 1, 4.72f, 11.52f, 6.41f, 12.78f},
-        {256, 256, 1, 8.50f, 23.79f, 10.43f, 23.49f},
+        {16, 16, 3, 0.39f, 1.39f, 0.75f, 2.52f},    {16, 16, 2, 0.56f, 1.06f, 1.57f, 2.53f},
+        {16, 32, 2, 0.60f, 1.33f, 1.66f, 3.36f},    {32, 32, 2, 0.58f, 2.61f, 1.14f, 3.59f},
+        {64, 32, 1, 0.91f, 2.38f, 1.56f, 2.61f},    {64, 64, 2, 0.90f, 4.80f, 1.62f, 6.69f},
+        {64, 64, 1, 1.32f, 3.94f, 2.37f, 3.69f},    {128, 64, 2, 0.89f, 6.66f, 2.05f, 10.17f},
+        {128, 64, 1, 1.89f, 5.50f, 2.68f, 5.46f},   {128, 128, 2, 1.27f, 13.25f, 4.04f, 15.88f},
+        {128, 128, 1, 2.74f, 8.41f, 3.57f, 9.25f},  {256, 128, 1, 5.34f, 11.83f, 6.43f, 12.30f},
+        {256, 256, 1, 9.16f, 23.49f, 10.36f, 22.82f},
     };
     return by_columns(kShapes, args, [&](int shape, const LinearArgs &a) {
         switch (shape) {
         case 0: return launch_tile<Tile<false, 16, 16, 16, 16, 256, 3, 4>>(a, stream);
         case 1: return launch_tile<Tile<false, 16, 16, 16, 16, 256, 4, 8, true>>(a, stream);
         case 2: return launch_tile<Tile<false, 16, 32, 16, 16, 256, 3, 4, true>>(a, stream);
-        case 3: return launch_tile<Tile<false, 64, 32, 16, 32, 256, 3, 4, true>>(a, stream);
-        case 4: return launch_tile<Tile<false, 64, 64, 32, 32, 64, 4>>(a, stream);
-        case 5: return launch_tile<Tile<false, 64, 64, 32, 32, 128, 4, 4, true>>(a, stream);
-        case 6: return launch_tile<Tile<false, 128, 64, 32, 32, 64, 3>>(a, stream);
-        case 7: return launch_tile<Tile<false, 128, 64, 32, 32, 128, 3, 4, true>>(a, stream);
-        case 8: return launch_tile<Tile<false, 128, 128, 32, 64, 64, 4, 4, true>>(a, stream);
-        case 9: return launch_tile<Tile<false, 256, 128, 64, 64, 64, 3, 4, true>>(a, stream);
+        case 3: return launch_tile<Tile<false, 32, 32, 16, 16, 256, 2, 4, true>>(a, stream);
+        case 4: return launch_tile<Tile<false, 64, 32, 16, 32, 256, 3, 4, true>>(a, stream);
+        case 5: return launch_tile<Tile<false, 64, 64, 32, 32, 64, 4>>(a, stream);
+        case 6: return launch_tile<Tile<false, 64, 64, 32, 32, 128, 4, 4, true>>(a, stream);
+        case 7: return launch_tile<Tile<false, 128, 64, 32, 32, 64, 3>>(a, stream);
+        case 8: return launch_tile<Tile<false, 128, 64, 32, 32, 128, 3, 4, true>>(a, stream);
+        case 9: return launch_tile<Tile<false, 128, 128, 32, 64, 64, 2>>(a, stream);
+        case 10: return launch_tile<Tile<false, 128, 128, 32, 64, 64, 4, 4, true>>(a, stream);
+        case 11: return launch_tile<Tile<false, 256, 128, 64, 64, 64, 3, 4, true>>(a, stream);
         default: return launch_tile<Tile<false, 256, 256, 128, 64, 64, 2>>(a, stream);
         }
     });

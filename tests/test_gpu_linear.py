@@ -46,7 +46,10 @@ TILES = [(1, 17, 1000), (1, 4100, 40), (1, 4100, 136), (33, 4100, 40), (33, 4100
          (2049, 4100, 1000), (513, 16001, 520), (2049, 10300, 264), (4097, 6001, 520),
          (4097, 1000, 136), (2049, 1000, 520), (400, 10300, 136), (4097, 4100, 40),
          (4097, 1000, 40), (4097, 10300, 40), (33, 16001, 264), (1, 16001, 520),
-         (257, 16001, 136), (200, 8200, 264)]
+         (257, 16001, 136), (200, 8200, 264),
+         (129, 33000, 40), (129, 33000, 520), (700, 33000, 40), (4097, 2000, 72), (4097, 6001, 40),
+         (513, 16001, 1000), (513, 33000, 520), (1025, 10300, 520), (257, 16001, 520),
+         (33, 8200, 520), (400, 33000, 136)]
 
 
 @pytest.mark.parametrize("M,N,K", TILES)
