@@ -17,7 +17,8 @@
 // What bounds it, measured with copies that leave parts out: at 8192^3 the matrix
 // instructions and LDS reads alone take 784 us, the loads alone 703 us, together
 // 950 us (1160 TFLOP/s; the library's product on the same card 764 us); the
-// LDS serves both, 1.5 KB read per MFMA of a 64 x 128 wave tile. 8192 x 10304 x 2048
+// LDS serves both, 96 of its 128 bytes a cycle to the reads of 128 x 64 wave tiles and
+// 32 to the loads at the matrix cores' full rate. 8192 x 10304 x 2048
 // takes 305-310 us (1120 TFLOP/s; the library 360). At 256 x 2048 x 4096 (one 64 x 32 tile
 // per compute unit, one wave per SIMD) 10 us of loads and 12 us of reads and MFMAs give
 // 11.5 us with loading waves of their own. A few rows stream w: 1 row x 50280 x 2048 in
@@ -155,8 +156,9 @@ typedef __attribute__((address_space(3))) void lds_void;
 
 // A workgroup computes BM rows x BN columns, in (BM / WM) (BN / WN) waves of
 // WM x WN each (16 x 16 tiles). Both operands pass through LDS in tiles of 2 BK
-// bytes of k (BK bf16, BK / 2 fp32), S buffers in turn: the direct loads (global_load_lds, 16 bytes a lane) of the
-// S - 1 tiles ahead run while the matrix cores work on this one. NL waves issue
+// bytes of k (BK bf16, BK / 2 fp32), S buffers in turn: the direct loads
+// (global_load_lds, 16 bytes a lane) of the S - 1 tiles ahead run while the matrix
+// cores work on this one. NL waves issue
 // the loads; with APART waves of their own, where a compute unit has one small
 // tile and the issue of the loads would hold up its few MFMAs (256 x 2048 x 4096 in
 // 64 x 32 tiles: 15.5 us, 12.8 with eight loading waves, 11.6 with four apart).

@@ -13,9 +13,9 @@
 //
 // The best top_k in short steps after the pass, from what the softmax needs
 // anyway, the maxima of each lane's 32 elements of a chunk (a segment; kept in
-// LDS): the lanes form 128 groups (64 for a small top_k), the top_k-th largest of the groups' maxima
-// bounds the row's top_k-th best from below, and only the segments that reach
-// it are read again (for top_k = 20 about 25), a wave two at a time. The
+// LDS): the lanes form 128 groups (64 for a small top_k), the top_k-th largest of
+// the groups' maxima bounds the row's top_k-th best from below, and only the
+// segments that reach it are read again (for top_k = 20 about 25), a wave two at a time. The
 // candidates' places are counted. Keys (value, then lower index) are unique
 // 64-bit numbers, so the result does not depend on the order of any of this.
 // Masked elements are no candidates: when fewer than top_k are left, the lowest
@@ -64,7 +64,8 @@ struct Chunk<IoBF16> {
         uint32_t w[4];
 #pragma unroll
         for (int k = 0; k < 4; ++k)
-            w[k] = (__float_as_uint(f[2 * k]) >> 16) | (__float_as_uint(f[2 * k + 1]) & 0xffff0000u);
+            w[k] = (__float_as_uint(f[2 * k]) >> 16) |
+                   (__float_as_uint(f[2 * k + 1]) & 0xffff0000u);
         return make_uint4(w[0], w[1], w[2], w[3]);
     }
 };

@@ -99,7 +99,8 @@ def test_gated_norm_refusals(kw, skw, code):
 @pytest.mark.parametrize("kw,code", [
     (dict(T=-1), SHAPE), (dict(V=0), SHAPE), (dict(k=-1), SHAPE), (dict(k=11), SHAPE),
     (dict(V=100, k=65), UNSUP), (dict(V=2 ** 31 - 1), UNSUP), (dict(T=2 ** 31), UNSUP),
-    (dict(T=2 ** 24 - 7), UNSUP), (dict(dt=3), DTYPE), (dict(x=None), NULL), (dict(tok=None), NULL), (dict(lp=None), NULL),
+    (dict(T=2 ** 24 - 7), UNSUP), (dict(dt=3), DTYPE), (dict(x=None), NULL),
+    (dict(tok=None), NULL), (dict(lp=None), NULL),
     (dict(k=1, ids=None), NULL), (dict(k=1, tlp=None), NULL), (dict(x=A + 1), ALIGN),
     (dict(x=A + 2, dt=F32), ALIGN), (dict(T=0, x=None), OK)])
 def test_token_logprobs_refusals(kw, code):
