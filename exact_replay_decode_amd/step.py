@@ -6,7 +6,7 @@ As in api.py this is argument marshalling only: tensors are checked for
 device, dtype, layout and size, then their data pointers and a HIP stream are
 handed to the library. Calls run on the stream given, or on the current stream
 of their tensors' device. Outputs that the caller does not pass are allocated
-on that stream.
+on that stream. No call records gradients.
 """
 from __future__ import annotations
 
