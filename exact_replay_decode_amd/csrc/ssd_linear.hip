@@ -555,7 +555,7 @@ hipError_t linear_bf16(const LinearArgs &args, hipStream_t stream) {
         case 1: return launch_tile<Tile<false, 16, 16, 16, 16, 256, 4, 8, true>>(a, stream);
         case 2: return launch_tile<Tile<false, 16, 32, 16, 16, 256, 3, 4, true>>(a, stream);
         case 3: return launch_tile<Tile<false, 32, 32, 16, 16, 256, 2, 4, true>>(a, stream);
-        case 4: return launch_tile<Tile<false, 64, 32, 16, 32, 256, 3, 4, true>>(a, stream);
+        case 4: return launch_tile<Tile<false, 64, 32, 32, 16, 256, 3, 4, true>>(a, stream);
         case 5: return launch_tile<Tile<false, 64, 64, 32, 32, 64, 4>>(a, stream);
         case 6: return launch_tile<Tile<false, 64, 64, 32, 32, 128, 4, 4, true>>(a, stream);
         case 7: return launch_tile<Tile<false, 128, 64, 32, 32, 64, 3>>(a, stream);
