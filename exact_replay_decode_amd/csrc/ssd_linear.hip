@@ -559,9 +559,9 @@ hipError_t linear_bf16(const LinearArgs &args, hipStream_t stream) {
         case 5: return launch_tile<Tile<false, 64, 64, 32, 32, 64, 4>>(a, stream);
         case 6: return launch_tile<Tile<false, 64, 64, 32, 32, 128, 4, 4, true>>(a, stream);
         case 7: return launch_tile<Tile<false, 128, 64, 32, 32, 64, 3>>(a, stream);
-        case 8: return launch_tile<Tile<false, 128, 64, 32, 32, 128, 3, 4, true>>(a, stream);
+        case 8: return launch_tile<Tile<false, 128, 64, 64, 32, 128, 3, 4, true>>(a, stream);
         case 9: return launch_tile<Tile<false, 128, 128, 32, 64, 64, 2>>(a, stream);
-        case 10: return launch_tile<Tile<false, 128, 128, 32, 64, 64, 4, 4, true>>(a, stream);
+        case 10: return launch_tile<Tile<false, 128, 128, 64, 32, 64, 4, 4, true>>(a, stream);
         case 11: return launch_tile<Tile<false, 256, 128, 64, 64, 64, 3, 4, true>>(a, stream);
         default: return launch_tile<Tile<false, 256, 256, 128, 64, 64, 2>>(a, stream);
         }
