@@ -29,7 +29,8 @@ namespace {
 
 constexpr int kPlan = 1024;        // threads of the planning workgroup
 constexpr int kCopy = 256;         // threads of the copying workgroups
-constexpr int kPiece = 65536;      // bytes of state that one workgroup moves
+constexpr int kPiece = 32768;      // bytes of state that one workgroup moves: eight
+                                   // 16-byte pieces a thread, all in flight at once
 constexpr int kRowGroup = 16;      // buffered rows that one workgroup moves (a page
                                    // holds a multiple of 16 rows)
 

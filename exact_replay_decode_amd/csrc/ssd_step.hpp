@@ -31,7 +31,7 @@ struct LinearArgs {
     LinearSeg seg[3];
 };
 
-// Tiles of a product's launch at most: its threads (up to 576 a tile) are counted
+// Tiles of a product's launch at most: its threads (up to 768 a tile) are counted
 // in 32 bits. A size whose 128 x 128 tiles are no more than this has a kernel.
 constexpr int64_t kLinearMaxTiles = 1 << 22;
 
