@@ -455,7 +455,10 @@ __global__ __launch_bounds__(64 * C::WAVES) void k_linear_tile(LinearArgs a, int
 // fit; a single round that is not full fix1 and ns1 with one on each, in between by
 // the line through the two. In bf16 that counts no further down than the time of
 // the arrays at 5.2 TB/s (but a fiftieth of it, for shapes that are all bound by
-// them). The figures are fitted to 466 sizes in bf16 (1 to 8192 rows, 256 to 50280
+// them). In one round, where nothing runs beside it, the epilogue counts when output
+// rows do not start on 16 bytes (734 x 7643 x 320 against 7648 columns: 14.9 against
+// 12.0 us in 256 x 128 tiles, 11.7 against 10.3 in 128 x 128; fp32 does not notice).
+// The figures are fitted to 466 sizes in bf16 (1 to 8192 rows, 256 to 50280
 // columns, K 256 to 4096) and 400 in fp32 (half the K), with weights that come from
 // memory, as a model's do: the shape that they pick is 1.2 % (fp32 1.8 %) slower than
 // the best one in the mean.
@@ -466,7 +469,13 @@ struct Shape {
 };
 constexpr int kUnits = 256;
 
-inline float shape_time(const Shape &s, int64_t M, int64_t N, int64_t K, bool bf16) {
+struct Problem {
+    int64_t M, N, K;
+    bool bf16, ragged;       // inputs; output rows that are not 16-byte aligned
+};
+
+inline float shape_time(const Shape &s, const Problem &p) {
+    const int64_t M = p.M, N = p.N, K = p.K;
     const int64_t tiles = ((M + s.bm - 1) / s.bm) * ((N + s.bn - 1) / s.bn);
     if (tiles > kLinearMaxTiles)
         return INFINITY;
@@ -477,16 +486,18 @@ inline float shape_time(const Shape &s, int64_t M, int64_t N, int64_t K, bool bf
         t = (float)((tiles + round - 1) / round) * full;
     else if (s.fit > 1)
         t += (full - one) * (float)((tiles - 1) / kUnits) / (float)(s.fit - 1);
+    if (tiles <= round && p.ragged)
+        t += 6e-5f * (float)(s.bm * s.bn);
     const float bytes = 2.0f * ((float)N * (float)K + (float)M * (float)K + (float)M * (float)N);
-    return bf16 ? std::max(t, bytes / 5.2e6f) + 0.02f * t : t;
+    return p.bf16 ? std::max(t, bytes / 5.2e6f) + 0.02f * t : t;
 }
 
 template <int S>
-int best_shape(const Shape (&s)[S], int64_t M, int64_t N, int64_t K, bool bf16, float *time) {
+int best_shape(const Shape (&s)[S], const Problem &p, float *time) {
     int best = 0;
-    *time = shape_time(s[0], M, N, K, bf16);
+    *time = shape_time(s[0], p);
     for (int i = 1; i < S; ++i) {
-        const float t = shape_time(s[i], M, N, K, bf16);
+        const float t = shape_time(s[i], p);
         if (t < *time) {
             *time = t;
             best = i;
@@ -503,16 +514,24 @@ int best_shape(const Shape (&s)[S], int64_t M, int64_t N, int64_t K, bool bf16, 
 constexpr float kSecondLaunch = 2.0f;
 template <int S, class F>
 hipError_t by_columns(const Shape (&s)[S], LinearArgs a, F each) {
+    const LinearSeg &o = a.seg[0];   // (of several, the others are as wide or few columns)
+    const int bytes = o.bf16 ? 2 : 4;
+    const Problem all = {a.M, a.N, a.K, a.io_bf16 != 0,
+                         a.io_bf16 && ((uintptr_t)o.p % 16 != 0 ||
+                                       (int64_t)(o.n1 - o.n0) * bytes % 16 != 0)};
     float best, rest_time;
-    int first = best_shape(s, a.M, a.N, a.K, a.io_bf16, &best), second = 0;
+    int first = best_shape(s, all, &best), second = 0;
     int64_t n1 = a.N;
     for (int i = 0; i < S; ++i) {
         const int64_t mt = (a.M + s[i].bm - 1) / s[i].bm, nt = (a.N + s[i].bn - 1) / s[i].bn;
         const int64_t round = kUnits * s[i].fit, cols = mt * nt / round * round / mt * s[i].bn;
         if (cols <= 0 || cols >= a.N)
             continue;
-        const int j = best_shape(s, a.M, a.N - cols, a.K, a.io_bf16, &rest_time);
-        const float t = shape_time(s[i], a.M, cols, a.K, a.io_bf16) + rest_time + kSecondLaunch;
+        Problem part = all, rest = all;
+        part.N = cols;
+        rest.N = a.N - cols;
+        const int j = best_shape(s, rest, &rest_time);
+        const float t = shape_time(s[i], part) + rest_time + kSecondLaunch;
         if (t < best) {
             best = t;
             first = i;
