@@ -253,3 +253,20 @@ def test_rows_past_32_bits(M, N, K):
     y = erd.ssd_linear(x, w, activation="relu2")
     for a in (0, M // 2, M - 3):
         assert same_bits(y[a:a + 3], erd.ssd_linear(x[a:a + 3], w, activation="relu2"))
+
+
+@pytest.mark.parametrize("M,N", [(2 ** 29 - 3, 8), (8, 2 ** 29 - 8)])
+def test_the_most_rows_and_columns(M, N):
+    """One dimension at the limit of a launch: rows (columns) far apart, the
+    last ones among them, against a call of their own."""
+    g = gen(N % 97)
+    x = torch.zeros(M, 8, dtype=torch.bfloat16, device=DEV)
+    w = torch.zeros(N, 8, dtype=torch.bfloat16, device=DEV)
+    at = torch.tensor([0, 1, 12345678, 2 ** 28 + 77, 2 ** 29 - 9], device=DEV)
+    few, many = (w, x) if M > N else (x, w)
+    few.copy_(randn(g, 8, 8))
+    many[at] = randn(g, 5, 8, dtype=torch.bfloat16)
+    y = erd.ssd_linear(x, w)
+    part = erd.ssd_linear(x[at], w) if M > N else erd.ssd_linear(x, w[at])
+    assert same_bits(y[at] if M > N else y[:, at].contiguous(), part)
+    assert int((y.view(-1).view(torch.int32) != 0).sum()) <= 5 * 8

@@ -206,3 +206,23 @@ def test_refusals_and_empty():
         erd.ssd_token_logprobs(x.half(), tok)
     with pytest.raises(ValueError, match="contiguous"):
         erd.ssd_token_logprobs(torch.zeros(10, 3, device=DEV).t(), tok)
+
+
+def test_the_most_rows():
+    """As many rows as a launch takes."""
+    T, V = 16777208, 3
+    g = gen(11)
+    x = randn(g, T, V, dtype=torch.bfloat16)
+    tok = torch.randint(0, V, (T,), generator=g, device=DEV, dtype=torch.int32)
+    r = erd.ssd_token_logprobs(x, tok, top_k=2)
+    for a in (0, T // 2 + 1, T - 700):
+        part = erd.ssd_token_logprobs(x[a:a + 700], tok[a:a + 700], top_k=2)
+        for p, w in zip(part, r):
+            assert same_bits(p, w[a:a + 700])
+    want = torch.log_softmax(x[-700:].double(), 1).gather(1, tok[-700:, None].long())[:, 0]
+    # (two chunks' worth of roundings bound three terms: 16 * 2**-24 and 2**-23 |lp|)
+    assert bool(((r.logprob[-700:].double() - want).abs()
+                 <= 16 * 2.0 ** -24 + 2.0 ** -23 * want.abs()).all())
+    with pytest.raises(erd.SsdError, match="UNSUPPORTED"):
+        erd.ssd_token_logprobs(torch.zeros(T + 1, 1, device=DEV),
+                               torch.zeros(T + 1, dtype=torch.int32, device=DEV))

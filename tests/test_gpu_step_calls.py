@@ -261,6 +261,26 @@ def test_lists_with_skipped_and_empty_entries():
     assert all(same_bits(x, y) for x, y in zip(_arrays(c), before))
 
 
+def test_the_longest_lists():
+    """As many entries as a launch takes, all but a few out of range."""
+    i32 = dict(dtype=torch.int32, device=DEV)
+    n = 16777208
+    (sh, c), (_, d) = _cache(7), _cache(7)
+    at = torch.tensor([5, n // 2, n - 1], device=DEV)
+    src, dst = torch.full((n,), -1, **i32), torch.full((n,), 9, **i32)
+    src[at], dst[at] = torch.tensor([2, 3, 5], **i32), torch.tensor([0, 1, 4], **i32)
+    small = [t[at].contiguous() for t in (src, dst)]
+    copied = torch.ones(n, **i32)
+    for k, (s, t), got in ((c, (src, dst), copied), (d, small, None)):
+        erd.ssd_replay_cache_free(sh, k, slot_idx=t)
+        ok = erd.ssd_replay_pages_reserve(sh, k, 1, slot_idx=t, like_idx=s)
+        assert int(ok.sum()) == 3
+        erd.ssd_replay_cache_copy(sh, k, k, t, s, copied=got)
+        erd.ssd_replay_pages_trim(sh, k, slot_idx=t)
+    assert int(copied.sum()) == 3 and bool(copied[at].all())
+    assert all(same_bits(x, y) for x, y in zip(_arrays(c), _arrays(d)))
+
+
 def test_outputs_given():
     a = Calls("f32", 20).fill(3)
     z, xBC, dt, h, o, logits, *score = a.run()
