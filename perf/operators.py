@@ -208,9 +208,9 @@ def _prepare_cache(s, c, g):
         s["ended"] = order[c["sources"] + n:c["sources"] + n + c["ended"]].contiguous()
         held[s["dst"].long()] = 0
     s["table"] = torch.where(at < held, perm, -1).to(torch.int32)
-    if c["op"] == "compact":
-        # the table as the run left it: a pass moves pages and rewrites the table, and the next
-        # pass begins from this one again
+    if c["op"] in ("fork", "compact"):
+        # the table as the run left it: a pass hands out or moves pages and rewrites the table,
+        # and the next pass begins from this one again
         s["before"] = s["table"].clone()
 
 
@@ -314,6 +314,7 @@ def _plain_reserve(s, slots, like, tokens):
 def _plain_fork(s):
     c = s["case"]
     ended, src, dst = (s[k].long() for k in ("ended", "src", "dst"))
+    s["table"].copy_(s["before"])
     s["table"][ended] = -1
     for name in ("state", "state_bf", "buf_len", "boundary_pos"):
         s[name][ended] = 0
@@ -399,6 +400,7 @@ def _own(s, c, op):
         granted = erd.ssd_replay_pages_reserve(shape, cache, s["tokens"], slot_idx=s["order"])
         return {"granted": granted, "table": s["table"]}
     if op == "fork":
+        s["table"].copy_(s["before"])
         erd.ssd_replay_cache_free(shape, cache, slot_idx=s["ended"])
         granted = erd.ssd_replay_pages_reserve(shape, cache, 0, slot_idx=s["dst"],
                                                like_idx=s["src"])
