@@ -37,9 +37,10 @@
 namespace ssd {
 namespace {
 
-constexpr int kStreams = 16;
+constexpr int kStreams = kLogprobStreams;
 constexpr int kPerLane = 32;
 constexpr int kChunkElems = 64 * kPerLane;
+static_assert(kChunkElems == kLogprobChunk, "a wave's chunk");
 constexpr int kSegs = 1024;       // segments read again
 constexpr int kCands = 1024;      // candidates (top_k = 64: 90 in the mean)
 
@@ -566,15 +567,10 @@ void k_logprobs(LogprobArgs a) {
     }
 }
 
-// 16 waves a row while all rows run at the same time (bf16 two to a compute unit: 512
-// rows of 50280 with top 8 in 18 against 24 us, 1024 in 33 against 33, 2048 in 62 against
-// 52; fp32 one: 256 rows in 14 against 18 us, 512 in 28 against 25), and in bf16 where
-// every wave has four chunks or more (2048 rows of 131072 with top 8: 102 against 108 us).
 template <class IO>
 hipError_t logprobs_impl(const LogprobArgs &a, hipStream_t stream) {
-    constexpr bool BF = sizeof(typename IO::T) == 2;
     const dim3 grid((unsigned)a.T);
-    if (a.T <= (BF ? 512 : 256) || (BF && a.V >= 4 * kStreams * kChunkElems)) {
+    if (logprob_waves(a.T, a.V, sizeof(typename IO::T) == 2) == 16) {
         if (a.k > 0)
             k_logprobs<IO, 16, true><<<grid, dim3(1024), 0, stream>>>(a);
         else

@@ -193,7 +193,8 @@ int ssd_token_logprobs(int64_t T, int64_t V, int32_t dtype, const void *logits,
         return SSD_ERR_DTYPE;
     if (T < 0 || V < 1 || top_k < 0 || top_k > V)
         return SSD_ERR_SHAPE;
-    // (indices up to a chunk past V stay within 32 bits, as do 256 threads a row)
+    // (indices up to a chunk past V stay within 32 bits, as do 256 threads a row; a row
+    // gets 1024 only where those do too)
     if (T > kMaxList || V > kMaxI32 - 65536 || top_k > 64)
         return SSD_ERR_UNSUPPORTED;
     if (T == 0)
