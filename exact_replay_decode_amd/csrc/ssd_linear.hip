@@ -180,6 +180,7 @@ struct Tile {
     static constexpr int RPL = 64 / PIECES;               // rows of one direct load
     static constexpr int LX = BM / RPL / NL, LW = BN / RPL / NL;   // loads per wave
     static constexpr int BYTES = (BM + BN) * BK * 2, XBYTES = BM * BK * 2;
+    static_assert(PIECES >= 8, "a row of the tile covers all eight places of swizzle()");
     static_assert(BM % (RPL * NL) == 0 && BN % (RPL * NL) == 0, "loads divide over the waves");
     static_assert(S * BYTES <= 160 * 1024, "LDS of a compute unit");
 };
@@ -203,11 +204,8 @@ __device__ __forceinline__ void loads_barrier() {
 }
 
 // What a row's pieces are exchanged by: eight rows that are read together
-// cover the 128 bytes of a bank row (rows of 64 bytes: in pairs).
-template <class C>
-__device__ __forceinline__ int swizzle(int row) {
-    return C::PIECES >= 8 ? row & 7 : (row >> 1) & 3;
-}
+// cover the 128 bytes of a bank row.
+__device__ __forceinline__ int swizzle(int row) { return row & 7; }
 
 template <class C>
 struct TileLoader {
@@ -234,7 +232,7 @@ struct TileLoader {
     // Byte offset of the lane's piece of load number i of an operand.
     __device__ static __forceinline__ int piece(int i, int lane) {
         const int row = i * C::RPL + lane / C::PIECES;
-        return (lane % C::PIECES) ^ swizzle<C>(row);
+        return (lane % C::PIECES) ^ swizzle(row);
     }
     __device__ static __forceinline__ uint32_t offset(int i, int lane, int last, uint32_t rb) {
         const int row = i * C::RPL + lane / C::PIECES;
@@ -306,7 +304,7 @@ __device__ __forceinline__ void tile_steps(const char *buf, f32x4 (&acc)[C::FM][
     const int r = lane & 15;
     const char *px = buf + ((wave % C::NWM) * C::WM + r) * (2 * C::BK);
     const char *pw = buf + C::XBYTES + ((wave / C::NWM) * C::WN + r) * (2 * C::BK);
-    const auto piece = [&](int kk) { return 16 * ((4 * (k0 + kk) + (lane >> 4)) ^ swizzle<C>(r)); };
+    const auto piece = [&](int kk) { return 16 * ((4 * (k0 + kk) + (lane >> 4)) ^ swizzle(r)); };
     u32x4 x[RX][G], w[RW][C::FN];
     const auto fragment = [&](const char *p, int kk) {
         u32x4 f = *reinterpret_cast<const u32x4 *>(p + piece(kk));
