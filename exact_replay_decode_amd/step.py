@@ -3,8 +3,9 @@
 probabilities of tokens, and the pages and slots of a replay cache.
 
 As in api.py this is argument marshalling only: tensors are checked for
-device, dtype, layout and size, then their data pointers and a HIP stream are
-handed to the library. Calls run on the stream given, or on the current stream
+device, dtype, layout and size, and outputs that the caller passes for memory
+of their own; then their data pointers and a HIP stream are handed to the
+library. Calls run on the stream given, or on the current stream
 of their tensors' device. Outputs that the caller does not pass are allocated
 on that stream. No call records gradients.
 """
@@ -56,6 +57,31 @@ def _chk(t, name, shape, dtype, device):
     return _need(t, name, shape, dtype, device)
 
 
+def _apart(outs, ins, same=()):
+    """Refuses outputs that share memory with one another or with what the
+    call reads (names with tensors; None and empty ones pass). same: names of
+    inputs that the output (of the same size then) may be itself."""
+    seen = []
+    for name, t in outs:
+        if t is None:
+            continue
+        a = t.data_ptr()
+        b = a + t.nbytes
+        for c, d, other in seen:
+            if a < d and c < b:
+                raise ValueError(f"{other} and {name} share memory")
+        if a < b:
+            seen.append((a, b, name))
+    for name, t in ins:
+        if t is None:
+            continue
+        a = t.data_ptr()
+        b = a + t.nbytes
+        for c, d, other in seen:
+            if a < d and c < b and a < b and not (a == c and b == d and name in same):
+                raise ValueError(f"{other} shares memory with {name}")
+
+
 def _io(t, name):
     if t.dtype not in _CODE:
         raise ValueError(f"{name}: dtype {t.dtype} is not bfloat16 or float32")
@@ -102,8 +128,12 @@ def ssd_linear(x, weight, bias=None, activation="none", residual=None, out=None,
         out_dtype = x.dtype if out is None else out.dtype
     if out_dtype not in _CODE:
         raise ValueError(f"out_dtype {out_dtype} is not bfloat16 or float32")
-    out = _new((M, N), (N, 1), dtype=out_dtype, device=dev) if out is None else \
+    if out is None:
+        out = _new((M, N), (N, 1), dtype=out_dtype, device=dev)
+    else:
         _chk(out, "out", (M, N), out_dtype, dev)
+        _apart((("out", out),), (("x", x), ("weight", weight), ("bias", bias),
+                                 ("residual", residual)), ("residual",))
     rc = _lib.load().ssd_linear(M, N, K, io, _CODE[out_dtype], _lib.ACTIVATIONS[activation],
                                 x.data_ptr(), weight.data_ptr(), _p(bias), _p(residual),
                                 out.data_ptr(), _raw_stream(dev.index))
@@ -139,6 +169,8 @@ def ssd_in_proj(shape: Shape, u, weight, bias=None, out=None, stream=None):
         _chk(z, "z", (M, H, P), io, dev)
         _chk(xBC, "xBC", (M, cd), io, dev)
         _chk(dt, "dt", (M, H), dtt, dev)
+        _apart((("z", z), ("xBC", xBC), ("dt", dt)),
+               (("u", u), ("weight", weight), ("bias", bias)))
     rc = _lib.load().ssd_in_proj(_shape(shape), M, K, u.data_ptr(), weight.data_ptr(), _p(bias),
                                  z.data_ptr(), xBC.data_ptr(), dt.data_ptr(),
                                  _raw_stream(dev.index))
@@ -161,8 +193,11 @@ def ssd_gated_norm(shape: Shape, y, weight, z=None, groups=None, eps=1e-5,
     _chk(weight, "weight", (shape.H * shape.P,), torch.float32, dev)
     if z is not None:
         _chk(z, "z", full, io, dev)
-    out = torch.empty_like(y) if out is None else \
+    if out is None:
+        out = torch.empty_like(y)
+    else:
         _chk(out, "out", full, io, dev)
+        _apart((("out", out),), (("y", y), ("z", z), ("weight", weight)), ("y", "z"))
     rc = _lib.load().ssd_gated_norm(_shape(shape), full[0],
                                     shape.G if groups is None else int(groups), float(eps),
                                     int(bool(norm_before_gate)), y.data_ptr(), _p(z),
@@ -213,6 +248,8 @@ def ssd_token_logprobs(logits, tokens, top_k=0, out: TokenLogprobs | None = None
         if k > 0:
             _chk(out.top_ids, "top_ids", (T, k), torch.int32, dev)
             _chk(out.top_logprobs, "top_logprobs", (T, k), torch.float32, dev)
+        _apart(zip(out._fields, out[:5 if k > 0 else 3]),
+               (("logits", logits), ("tokens", tokens)))
     rc = _lib.load().ssd_token_logprobs(
         T, V, code, logits.data_ptr(), tokens.data_ptr(), k, out.logprob.data_ptr(),
         _p(out.entropy), _p(out.rank), _p(out.top_ids), _p(out.top_logprobs),
@@ -254,8 +291,14 @@ def ssd_replay_pages_reserve(shape: Shape, cache: ReplayCache, tokens, slot_idx=
         tok, every = _chk(tokens, "tokens", (n,), torch.int32, dev).data_ptr(), 0
     else:
         tok, every = None, max(0, min(int(tokens), shape.chunk_size))
-    granted = _new((n,), (1,), dtype=torch.int32, device=dev) if granted is None else \
+    if granted is None:
+        granted = _new((n,), (1,), dtype=torch.int32, device=dev)
+    else:
         _chk(granted, "granted", (n,), torch.int32, dev)
+        _apart((("granted", granted),),
+               (("tokens", None if tok is None else tokens), ("slot_idx", slot_idx),
+                ("like_idx", like_idx), ("buf_pages", cache.buf_pages),
+                ("buf_len", cache.buf_len)))
     rc = _lib.load().ssd_replay_pages_reserve(_shape(shape), cs, n, sl, _p(like), tok, every,
                                               granted.data_ptr(), _raw_stream(dev.index))
     _lib.check(rc, "ssd_replay_pages_reserve")
@@ -304,6 +347,10 @@ def ssd_replay_cache_copy(shape: Shape, dst: ReplayCache, src: ReplayCache, dst_
     _chk(src_idx, "src_idx", (n,), torch.int32, dev)
     if copied is not None:
         _chk(copied, "copied", (n,), torch.int32, dev)
+        _apart((("copied", copied),),
+               (("dst_idx", dst_idx), ("src_idx", src_idx), ("dst.buf_pages", dst.buf_pages),
+                ("src.buf_pages", src.buf_pages), ("dst.buf_len", dst.buf_len),
+                ("src.buf_len", src.buf_len)))
     rc = _lib.load().ssd_replay_cache_copy(_shape(shape), cd, cs, n, dst_idx.data_ptr(),
                                            src_idx.data_ptr(), _p(copied),
                                            _raw_stream(dev.index))
@@ -321,12 +368,15 @@ def ssd_replay_pages_compact(shape: Shape, cache: ReplayCache, used=None, worksp
             return ssd_replay_pages_compact(shape, cache, used, workspace)
     lib = _lib.load()
     words = lib.ssd_replay_pages_compact_workspace_bytes(cs) // 4
+    given = used is not None or workspace is not None
     used = _new((1,), (1,), dtype=torch.int32, device=dev) if used is None else \
         _chk(used, "used", (1,), torch.int32, dev)
     if workspace is None:
         workspace = _new((words,), (1,), dtype=torch.int32, device=dev)
     else:
         _chk(workspace, "workspace", (words,), torch.int32, dev)
+    if given:
+        _apart((("used", used), ("workspace", workspace)), (("buf_pages", cache.buf_pages),))
     rc = lib.ssd_replay_pages_compact(_shape(shape), cs, used.data_ptr(), workspace.data_ptr(),
                                       4 * words, _raw_stream(dev.index))
     _lib.check(rc, "ssd_replay_pages_compact")
