@@ -88,6 +88,14 @@ def _io(t, name):
     return _CODE[t.dtype]
 
 
+def _i32(v, name):
+    """A count for an int32 argument, which ctypes would cut to 32 bits."""
+    v = int(v)
+    if not -2 ** 31 <= v < 2 ** 31:
+        raise ValueError(f"{name}: {v} does not fit 32 bits")
+    return v
+
+
 def _p(t):
     return None if t is None else t.data_ptr()
 
@@ -199,8 +207,8 @@ def ssd_gated_norm(shape: Shape, y, weight, z=None, groups=None, eps=1e-5,
         _chk(out, "out", full, io, dev)
         _apart((("out", out),), (("y", y), ("z", z), ("weight", weight)), ("y", "z"))
     rc = _lib.load().ssd_gated_norm(_shape(shape), full[0],
-                                    shape.G if groups is None else int(groups), float(eps),
-                                    int(bool(norm_before_gate)), y.data_ptr(), _p(z),
+                                    shape.G if groups is None else _i32(groups, "groups"),
+                                    float(eps), int(bool(norm_before_gate)), y.data_ptr(), _p(z),
                                     weight.data_ptr(), out.data_ptr(), _raw_stream(dev.index))
     _lib.check(rc, "ssd_gated_norm")
     return out
@@ -231,7 +239,7 @@ def ssd_token_logprobs(logits, tokens, top_k=0, out: TokenLogprobs | None = None
     code = _io(logits, "logits")
     _chk(logits, "logits", (T, V), logits.dtype, dev)
     _chk(tokens, "tokens", (T,), torch.int32, dev)
-    k = int(top_k)
+    k = _i32(top_k, "top_k")
     if out is None:
         f, i = torch.float32, torch.int32
         out = TokenLogprobs(
@@ -269,7 +277,7 @@ def _list(slot_idx, cache, device):
     """(entries, slot list) of a call over slot_idx (None: every slot)."""
     if slot_idx is None:
         return cache.num_slots, None
-    n = slot_idx.shape[0]
+    n = _i32(slot_idx.shape[0], "slot_idx")
     return n, _chk(slot_idx, "slot_idx", (n,), torch.int32, device).data_ptr()
 
 
@@ -342,7 +350,7 @@ def ssd_replay_cache_copy(shape: Shape, dst: ReplayCache, src: ReplayCache, dst_
     if not _here(dev, stream):
         with _elsewhere(dev, stream):
             return ssd_replay_cache_copy(shape, dst, src, dst_idx, src_idx, copied)
-    n = dst_idx.shape[0]
+    n = _i32(dst_idx.shape[0], "dst_idx")
     _chk(dst_idx, "dst_idx", (n,), torch.int32, dev)
     _chk(src_idx, "src_idx", (n,), torch.int32, dev)
     if copied is not None:

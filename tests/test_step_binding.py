@@ -143,3 +143,18 @@ def test_page_calls_write_no_list(lib):
             workspace=work[:14])
     refused(lib, "used shares memory with buf_pages", compact, SH, c,
             used=c.buf_pages.view(-1)[:1])
+
+
+def test_counts_past_32_bits_are_refused(lib):
+    sh = erd.Shape(4, 2, 16, 16, 64, "f32", "f32")
+    y, w = torch.zeros(2, 4, 16), torch.zeros(64)
+    served(lib, erd.ssd_gated_norm, sh, y, w, groups=2)
+    refused(lib, "32 bits", erd.ssd_gated_norm, sh, y, w, groups=2 ** 32 + 2)
+    logits, tok = torch.zeros(1, 8), torch.zeros(1, dtype=I32)
+    served(lib, erd.ssd_token_logprobs, logits, tok, 1)
+    for k in (2 ** 32 + 1, -2 ** 32 + 1):
+        refused(lib, "32 bits", erd.ssd_token_logprobs, logits, tok, k)
+    c = erd.ReplayCache(SH, 3, "cpu")
+    long = torch.zeros(1, dtype=I32).expand(2 ** 32 + 1)      # (takes no memory)
+    refused(lib, "32 bits", erd.ssd_replay_cache_free, SH, c, slot_idx=long)
+    refused(lib, "32 bits", erd.ssd_replay_cache_copy, SH, c, c, long, long)
