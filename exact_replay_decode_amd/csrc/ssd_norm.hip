@@ -73,10 +73,9 @@ struct Eight<IoF32> {
     }
 };
 
-// SiLU with the hardware exp2 and reciprocal (an ulp each, far below the bf16
-// rounding; 1 / inf is 0).
+template <class IO>
 __device__ __forceinline__ float silu(float z) {
-    return z * __builtin_amdgcn_rcpf(1.0f + __expf(-z));
+    return z * (sizeof(typename IO::T) == 2 ? sigmoid_bf16(z) : sigmoid_f32(z));
 }
 
 // The lane's pieces of one group, lanes apart: the gated values and their sum of
@@ -101,7 +100,7 @@ struct Pieces {
             if (c < a.gs) {
 #pragma unroll
                 for (int j = 0; j < 8; ++j) {
-                    g[i][j] = a.z ? silu(g[i][j]) : 1.0f;
+                    g[i][j] = a.z ? silu<IO>(g[i][j]) : 1.0f;
                     if (!a.before)
                         v[i][j] *= g[i][j];
                     sum = fmaf(v[i][j], v[i][j], sum);

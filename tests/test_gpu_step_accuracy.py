@@ -39,3 +39,19 @@ def test_silu_and_gelu_of_an_fp32_output(io, M):
     near = arg > -87.0
     bound = U * (9 + 5 * arg.clamp(max=0.0).abs())
     assert bool((relative(y[:, 1], activate64(v, "gelu")) <= bound)[near].all())
+
+
+@pytest.mark.parametrize("H", [4, 32, 160])
+def test_gate_of_an_fp32_norm(H):
+    """Norm first, gate after, on rows of ones with weights of ones: r is the
+    same for every element, 1 / sqrt(1 + eps) within 6 u (the sum of ones is
+    exact, the division, eps, the sum and the reciprocal root, an ulp, round; half
+    their error passes the root), the gate within 8 u (7 u and its product), two
+    more products."""
+    sh = erd.Shape(H, 1, 64, 128, 256, "f32", "f32")
+    n = H * 64
+    z = torch.linspace(-87.0, 20.0, 2 * n, device=DEV).view(2, H, 64)
+    out = erd.ssd_gated_norm(sh, torch.ones_like(z), torch.ones(n, device=DEV), z=z, groups=1,
+                             eps=1e-5, norm_before_gate=True)
+    ref = activate64(z.double(), "silu") / math.sqrt(1 + 1e-5)
+    assert float(relative(out, ref).max()) <= 17 * U
