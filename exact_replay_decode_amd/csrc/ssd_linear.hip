@@ -2,11 +2,11 @@
 // epilogue: the mixer's projections (and any other linear layer of a step).
 //   out[m][n] = act(sum_k x[m][k] w[n][k] + bias[n]) + residual[m][n]
 //
-// Every output is one fp32 accumulation chain of matrix-core instructions over
+// Every output is an fp32 accumulation chain of matrix-core instructions over
 // 64-byte steps of k, ascending from zero: one v_mfma_f32_16x16x32_bf16 for the
 // step's 32 k in bf16, four v_mfma_f32_16x16x4_f32 for its 16 k in fp32 (the
-// i-th takes k = i, 4 + i, 8 + i, 12 + i of the step); k past K are zeros on
-// both sides. An MFMA result element depends on its own row, its own column
+// i-th takes k = i, 4 + i, 8 + i, 12 + i of the step), where a chain ends after 512 k
+// and the chains are added in turn; k past K are zeros on both sides. An MFMA result element depends on its own row, its own column
 // and its accumulator only, so every tile shape here gives the same bits, and
 // a row's bits do not depend on the number of rows. (The price is that k is
 // never split over waves that would add partial sums.)
@@ -157,6 +157,14 @@ __device__ __forceinline__ int wave_id() {
 
 typedef __attribute__((address_space(3))) void lds_void;
 
+// k of one fp32 chain. A longer sum is several, added in ascending order: the error of
+// a chain grows with the root of its length (64 x 64 x 16384 in one: 2.3e-6 of the
+// values' root mean square; in chains of 512, whatever K is: 4.1e-7), and where they
+// end depends on K alone. It costs 1-4 % of the time (256 x 2048 x 4096: 43.2 -> 44.9 us).
+// A bf16 step adds 32 products at a time; that stays one chain (1.8e-7 at K = 1024,
+// 8.3e-7 at 16384).
+constexpr int kChain = 512;
+
 // A workgroup computes BM rows x BN columns, in (BM / WM) (BN / WN) waves of
 // WM x WN each (16 x 16 tiles). Both operands pass through LDS in tiles of 2 BK
 // bytes of k (BK bf16, BK / 2 fp32), S buffers in turn: the direct loads
@@ -179,10 +187,14 @@ struct Tile {
     static constexpr int L0 = APART ? NW : 0;             // the first wave that loads
     static constexpr int WAVES = L0 + NL > NW ? L0 + NL : NW;
     static constexpr int FM = WM / 16, FN = WN / 16;
+    static constexpr int CHAIN = F32 ? 2 * kChain / BK : 0;   // tiles of a chain; 0: all
     static constexpr int PIECES = BK / 8;                 // 16-byte pieces of a row
     static constexpr int RPL = 64 / PIECES;               // rows of one direct load
     static constexpr int LX = BM / RPL / NL, LW = BN / RPL / NL;   // loads per wave
     static constexpr int BYTES = (BM + BN) * BK * 2, XBYTES = BM * BK * 2;
+    // fp32 (two sets of sums): registers for as many waves a SIMD as the LDS has room for
+    static constexpr int PER_SIMD = F32 ? 160 * 1024 / (S * BYTES) * WAVES / 4 : 1;
+    static_assert(!F32 || 2 * kChain % BK == 0, "chains end with a tile, in every shape alike");
     static_assert(PIECES >= 8, "a row of the tile covers all eight places of swizzle()");
     static_assert(BM % (RPL * NL) == 0 && BN % (RPL * NL) == 0, "loads divide over the waves");
     static_assert(S * BYTES <= 160 * 1024, "LDS of a compute unit");
@@ -261,7 +273,10 @@ struct TileLoader {
     // of 2 bytes): pieces past the row fetch the tile's first piece instead, and
     // count as zeros when they are read.
     __device__ __forceinline__ void load_tail(char *buf, int64_t kb, int left) const {
-        const int lane = threadIdx.x & 63, wave = wave_id() - C::L0;
+        int lane = threadIdx.x & 63;
+        const int wave = wave_id() - C::L0;
+        if constexpr (C::F32)   // (no registers for these offsets through the loop before)
+            asm volatile("" : "+v"(lane));
         const uint32_t lds = (uint32_t)(uintptr_t)(lds_void *)buf;
         const auto at = [&](uint32_t off, int i) {
             const int p = piece(i, lane);
@@ -359,7 +374,7 @@ __device__ __forceinline__ bool tile_of(int b, int mtiles, int ntiles, int &m, i
 }
 
 template <class C>
-__global__ __launch_bounds__(64 * C::WAVES) void k_linear_tile(LinearArgs a, int mtiles,
+__global__ __launch_bounds__(64 * C::WAVES, C::PER_SIMD) void k_linear_tile(LinearArgs a, int mtiles,
                                                              int ntiles) {
     constexpr int S = C::S, BK = C::BK;
     __shared__ __attribute__((aligned(1024))) char buf[S * C::BYTES];
@@ -372,11 +387,21 @@ __global__ __launch_bounds__(64 * C::WAVES) void k_linear_tile(LinearArgs a, int
     const bool loads = C::NL == C::WAVES || (wave >= C::L0 && wave < C::L0 + C::NL);
     const bool works = C::NW == C::WAVES || wave < C::NW;
     const TileLoader<C> ld(a, m0, n0);
-    f32x4 acc[C::FM][C::FN] = {};
+    f32x4 acc[C::FM][C::FN] = {}, total[C::FM][C::FN] = {};
+    const auto end_chain = [&] {
+        asm volatile("");   // (a branch: selections would wait for the sums after each tile)
+#pragma unroll
+        for (int i = 0; i < C::FM; ++i)
+#pragma unroll
+            for (int j = 0; j < C::FN; ++j) {
+                total[i][j] += acc[i][j];
+                acc[i][j] = (f32x4){0.0f, 0.0f, 0.0f, 0.0f};
+            }
+    };
     const int k2 = a.K * (C::F32 ? 2 : 1);   // a row in units of 2 bytes
     const int full = k2 / BK, left = k2 % BK, tiles = full + (left != 0);
     const auto load = [&](int t, int slot) {
-        if (t < full)
+        if (C::F32 ? __builtin_expect(t < full, 1) : t < full)
             ld.load(buf + slot * C::BYTES, (int64_t)t * BK * 2);
         else
             ld.load_tail(buf + slot * C::BYTES, (int64_t)t * BK * 2, left);
@@ -400,6 +425,9 @@ __global__ __launch_bounds__(64 * C::WAVES) void k_linear_tile(LinearArgs a, int
             load(t + S - 1, ahead);
         if (works)
             tile_steps<C, BK / 32>(buf + slot * C::BYTES, acc);
+        if constexpr (C::CHAIN > 0)
+            if ((t + 1) % C::CHAIN == 0)
+                end_chain();
         slot = slot + 1 == S ? 0 : slot + 1;
         ahead = ahead + 1 == S ? 0 : ahead + 1;
     }
@@ -410,6 +438,9 @@ __global__ __launch_bounds__(64 * C::WAVES) void k_linear_tile(LinearArgs a, int
             for (int k = 0; k < left; k += 32)
                 tile_steps<C, 1, true>(buf + slot * C::BYTES, acc, k / 32, left);
     }
+    if constexpr (C::CHAIN > 0)
+        end_chain();
+    const auto &sum = *(C::CHAIN > 0 ? &total : &acc);
     __syncthreads();
     if (!works)
         return;
@@ -430,7 +461,7 @@ __global__ __launch_bounds__(64 * C::WAVES) void k_linear_tile(LinearArgs a, int
 #pragma unroll
             for (int j = 0; j < C::FN; ++j)
                 *reinterpret_cast<f32x4 *>(mine + (16 * i + (lane & 15)) * PITCH + 16 * j +
-                                           4 * (lane >> 4)) = acc[h * HALF + i][j];
+                                           4 * (lane >> 4)) = sum[h * HALF + i][j];
         __builtin_amdgcn_wave_barrier();
 #pragma unroll 1
         for (int e = lane; e < HALF * 16 * (C::WN / 8); e += 64) {

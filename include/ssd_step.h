@@ -38,9 +38,10 @@ typedef enum {
  *   residual  [M,N] io_dtype, or NULL
  *   out       [M,N] out_dtype (SSD_F32 or SSD_BF16); may be `residual`
  *             itself when the dtypes agree, and aliases nothing else
- * The sum is one fp32 chain over k in a fixed order (matrix-core steps of 32
- * k in bf16, of 4 in fp32; a bf16 product is exact in fp32), the epilogue is
- * fp32, and the result is rounded once. The bits of a row do not depend on M.
+ * The sum is an fp32 chain over k in a fixed order (matrix-core steps of 32
+ * k in bf16, of 4 in fp32, where every 512 k are a chain of their own and the
+ * chains are added in order; a bf16 product is exact in fp32), the epilogue
+ * is fp32, and the result is rounded once. The bits of a row do not depend on M.
  * M >= 0, N >= 0, K >= 1. K a multiple of 8 (bf16) or 4 (fp32) and at most
  * 1048576, and at most 4194304 tiles of 128 x 128 outputs, else
  * SSD_ERR_UNSUPPORTED. x and w 16-byte aligned (the others need their natural

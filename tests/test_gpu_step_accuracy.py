@@ -55,3 +55,35 @@ def test_gate_of_an_fp32_norm(H):
                              eps=1e-5, norm_before_gate=True)
     ref = activate64(z.double(), "silu") / math.sqrt(1 + 1e-5)
     assert float(relative(out, ref).max()) <= 17 * U
+
+
+@pytest.mark.parametrize("M,N", [(5, 40), (64, 64), (300, 520), (1100, 700)])
+def test_fp32_sums_are_chains_of_512(M, N):
+    """Worst case: a chain of 512 loses at most 512 half steps of its partial
+    sums, which sum |x w| bounds, and adding up the K / 512 chains one each. The
+    terms 1 + 11 2**-15 lose all but the 1 in a single chain that has passed
+    2**15: 11 of 65558, 1.7e-4, against the bound's 3.8e-5."""
+    K = 65536
+    x = torch.ones(M, K, device=DEV)
+    w = torch.full((N, K), 1 + 11 * 2.0 ** -15, device=DEV)
+    y = erd.ssd_linear(x, w)
+    ref = K * (1 + 11 * 2.0 ** -15)
+    assert float((y.double() - ref).abs().max()) <= (512 + K // 512 + 2) * U * ref
+
+
+@pytest.mark.parametrize("M,N", [(64, 64), (300, 520), (1100, 700)])
+@pytest.mark.parametrize("K", [512, 1000, 1024, 2056, 4096, 16384])
+def test_fp32_error_does_not_grow_with_k(M, N, K):
+    """Independent roundings, each of a root mean square of at most u / sqrt(3) of
+    the partial sum, on partial sums of random signs, whose mean square is j of
+    j terms: a chain of n has a mean square error of u^2 n^2 / 6, the chains of a
+    sum of K add up to u^2 512 K / 6, the K / 512 additions of chains to
+    u^2 (K / 512 + 1) K / 6, against the values' K. (One chain of 2056 would be
+    at 8e-7, of 16384 at 2.3e-6; this bound stays below 5.8e-7.)"""
+    g = torch.Generator(device=DEV)
+    g.manual_seed(K + M)
+    x, w = (torch.randn(n, K, generator=g, device=DEV) for n in (M, N))
+    y = erd.ssd_linear(x, w)
+    ref = x.double() @ w.double().t()
+    err = float((y.double() - ref).square().mean().sqrt() / ref.square().mean().sqrt())
+    assert err <= U * math.sqrt((min(K, 512) + K / 512 + 1) / 6)
