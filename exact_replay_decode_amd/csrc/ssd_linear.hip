@@ -42,25 +42,35 @@ typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
 
 // ---- epilogue ---------------------------------------------------------------
 
-// F32: for an fp32 output. (One branch for the eight: a switch for each of them and
-// full divisions cost 4 us of 20 in 256 x 128 tiles.)
-template <bool F32>
-__device__ __forceinline__ void activate(float (&v)[8], int act) {
-    if (act == SSD_ACT_SILU) {
-#pragma unroll
-        for (int i = 0; i < 8; ++i)
-            v[i] *= F32 ? sigmoid_f32(v[i]) : sigmoid_bf16(v[i]);
-    } else if (act == SSD_ACT_GELU) {
-        // 0.5 (1 + tanh(u)) = 1 / (1 + exp(-2u)), u = sqrt(2/pi)(v + 0.044715 v^3)
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            const float u2 = 1.5957691216057308f * fmaf(0.044715f * v[i] * v[i], v[i], v[i]);
-            v[i] *= F32 ? sigmoid_f32(u2) : sigmoid_bf16(u2);
-        }
-    } else if (act == SSD_ACT_RELU2) {
+// f32: for an fp32 output. (Branches for the eight together: a switch for each of them
+// and full divisions cost 4 us of 20 in 256 x 128 tiles.)
+__device__ __forceinline__ void activate(float (&v)[8], int act, bool f32) {
+    if (act == SSD_ACT_RELU2) {
 #pragma unroll
         for (int i = 0; i < 8; ++i)
             v[i] = v[i] <= 0.0f ? 0.0f : v[i] * v[i];   // (a NaN stays one)
+        return;
+    }
+    if (act != SSD_ACT_SILU && act != SSD_ACT_GELU)
+        return;
+    float u[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+        u[i] = v[i];
+    if (act == SSD_ACT_GELU) {
+        // 0.5 (1 + tanh(u)) = 1 / (1 + exp(-2u)), u = sqrt(2/pi)(v + 0.044715 v^3)
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+            u[i] = 1.5957691216057308f * fmaf(0.044715f * v[i] * v[i], v[i], v[i]);
+    }
+    if (f32) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+            v[i] *= sigmoid_f32(u[i]);
+    } else {
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+            v[i] *= sigmoid_bf16(u[i]);
     }
 }
 
@@ -116,10 +126,7 @@ __device__ __forceinline__ void store_eight(const LinearArgs &a, int m, int n, f
                                  : static_cast<const float *>(a.residual)[at + i];
         }
     }
-    if (s.bf16)
-        activate<false>(v, a.act);
-    else
-        activate<true>(v, a.act);
+    activate(v, a.act, !s.bf16);
     if (a.residual)
 #pragma unroll
         for (int i = 0; i < 8; ++i)
