@@ -210,12 +210,13 @@ struct Tile {
 // One direct load of 1 KB: lane l's 16 bytes from base + off to LDS byte
 // lds + 16 l. (An asm statement without register outputs: the compiler, which
 // cannot tell the buffers apart, would wait for all loads in flight before
-// each LDS read; the kernel waits at its barriers instead.)
+// each LDS read; the kernel waits at its barriers instead. m0 is an operand, so the
+// compiler keeps track of it; the load may not follow its writing at once.)
 __device__ __forceinline__ void direct_load(uint32_t lds, const char *base, uint32_t off) {
-    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, %2"
+    asm volatile("s_nop 0\n\tglobal_load_lds_dwordx4 %1, %2"
                  :
-                 : "s"(lds), "v"(off), "s"(base)
-                 : "m0", "memory");
+                 : "{m0}"(lds), "v"(off), "s"(base)
+                 : "memory");
 }
 
 // Waits for this wave's direct loads except the newest N and its LDS reads,
