@@ -17,13 +17,16 @@ namespace ssd {
 // fit; a single round that is not full fix1 and ns1 with one on each, in between by
 // the line through the two. In bf16 that counts no further down than the time of
 // the arrays at 5.2 TB/s (but a fiftieth of it, for shapes that are all bound by
-// them). In one round, where nothing runs beside it, the epilogue counts when output
-// rows do not start on 16 bytes (734 x 7643 x 320 against 7648 columns: 14.9 against
-// 12.0 us in 256 x 128 tiles, 11.7 against 10.3 in 128 x 128; fp32 does not notice).
+// them). In a single launch of one round, where nothing runs beside it, the epilogue
+// counts when output rows do not start on 16 bytes (734 x 7643 x 320 against 7648
+// columns: 14.9 against 12.0 us in 256 x 128 tiles, 11.7 against 10.3 in 128 x 128; fp32
+// does not notice). Of 200 drawn sizes with odd columns that changes the choice for 20,
+// at 0.81 to 1.05 of the time without it, 0.94 in the mean.
 // The figures are fitted to 466 sizes in bf16 (1 to 8192 rows, 256 to 50280
 // columns, K 256 to 4096) and 400 in fp32 (half the K), with weights that come from
-// memory, as a model's do: the shape that they pick is 1.2 % (fp32 1.8 %) slower than
-// the best one in the mean.
+// memory, as a model's do. On those above 6 us the shape that they pick is 1.2 % slower
+// than the best one in the mean in bf16 (7 % at the 95th percentile), 1.2 % (6 %) in
+// fp32. (profiles/linear_shapes_sweep.csv has every shape's time at each of them.)
 struct LinearShape {
     int bm, bn;
     int fit;                 // workgroups that run on a compute unit at a time
@@ -97,8 +100,11 @@ struct LinearPlan {
 // One launch over all columns, or one over the columns of a shape's whole rounds
 // and one, in a smaller shape, over the rest, where the last round would leave
 // most of the device idle (8192 x 10304 x 2048 in 256 x 256 tiles: 5 rounds and 32
-// tiles, 386 us; with the last 64 columns on their own 305).
-constexpr float kSecondLaunch = 2.0f;
+// tiles, 386 us; with the last 64 columns on their own 305; fp32 2048 x 10304 x 2048 715
+// and 637). What the second launch has to save, in us: of the sizes of the fit 39 take
+// two in bf16, at 0.94 of the one launch's time in the mean (0.77-1.12), 10 in fp32, at
+// 0.96 (0.87-1.09). With 2 us in fp32 it was 77, at 1.04.
+constexpr float kSecondLaunch[] = {15.0f, 4.0f};   // fp32, bf16
 template <int S>
 LinearPlan linear_plan(const LinearShape (&s)[S], const LinearProblem &all) {
     float best, rest_time;
@@ -110,10 +116,12 @@ LinearPlan linear_plan(const LinearShape (&s)[S], const LinearProblem &all) {
         if (cols <= 0 || cols >= all.N)
             continue;
         LinearProblem part = all, rest = all;
+        part.ragged = rest.ragged = false;   // (each runs beside the other)
         part.N = cols;
         rest.N = all.N - cols;
         const int j = best_linear_shape(s, rest, &rest_time);
-        const float t = linear_time(s[i], part) + rest_time + kSecondLaunch;
+        const float t = linear_time(s[i], part) + rest_time +
+                        kSecondLaunch[all.bf16];
         if (t < best) {
             best = t;
             plan = {i, j, cols};

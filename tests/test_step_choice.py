@@ -24,6 +24,7 @@ def test_tile_shapes_of_products(tmp_path):
     import subprocess
 
     from test_gpu_linear import TILES
+    from test_gpu_linear_plans import TWICE
     from test_native_sanitizers import CSRC, NATIVE, ROOT, _build_and_run
     _build_and_run(
         tmp_path, "g++", [os.path.join(NATIVE, "linear_choice_check.cpp")],
@@ -36,7 +37,11 @@ def test_tile_shapes_of_products(tmp_path):
         plans = [tuple(map(int, line.split()[1:])) for line in out.splitlines()
                  if line.startswith("plan")]
         assert len(plans) == len(TILES)
-        alone = {a for a, b in plans if b < 0}
         missing = set(range(shapes)) - {s for p in plans for s in p}
         assert not missing, (bf16, missing)
-        assert len({p for p in plans if p[1] >= 0}) >= 5 and len(alone) >= 5
+        assert len({a for a, b in plans if b < 0}) >= 5
+        sizes = "".join(f"{bf16} {M} {N} {K}\n" for M, N, K in TWICE[bf16])
+        out = subprocess.run([str(tmp_path / "linear_choice_check")], input=sizes,
+                             capture_output=True, text=True, timeout=60, check=True).stdout
+        twice = [line.split()[1:] for line in out.splitlines() if line.startswith("plan")]
+        assert len(twice) == len(TWICE[bf16]) and all(b != "-1" for _, b in twice), twice
