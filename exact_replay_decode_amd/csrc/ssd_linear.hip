@@ -8,21 +8,22 @@
 // i-th takes k = i, 4 + i, 8 + i, 12 + i of the step), where a chain ends after 512 k
 // and the chains are added in turn; k past K are zeros on both sides. An MFMA result element depends on its own row, its own column
 // and its accumulator only, so every tile shape here gives the same bits, and
-// a row's bits do not depend on the number of rows. (The price is that k is
-// never split over waves that would add partial sums.)
+// a row's bits do not depend on the number of rows. (A wave has all of k: work comes
+// from outputs alone, and few of them with a long k take the time of their sum.)
 //
 // The instruction's rows are output columns n and its columns are rows m of x:
 // a lane then holds four consecutive n of one row.
 //
-// What bounds it, measured with copies that leave parts out: at 8192^3 the matrix
-// instructions and LDS reads alone take 784 us, the loads alone 703 us, together
-// 950 us (1160 TFLOP/s; the library's product on the same card 764 us); the
+// What bounds it, measured with copies that leave parts out: at 8192^3 (uniform values)
+// the matrix instructions and LDS reads alone take 596 us, the loads alone 710,
+// together 835 (1320 TFLOP/s; normal values 835-890, the library's product 743-764); the
 // LDS serves both, 96 of its 128 bytes a cycle to the reads of 128 x 64 wave tiles and
 // 32 to the loads at the matrix cores' full rate. 8192 x 10304 x 2048
-// takes 305-310 us (1120 TFLOP/s; the library 360). At 256 x 2048 x 4096 (one 64 x 32 tile
-// per compute unit, one wave per SIMD) 10 us of loads and 12 us of reads and MFMAs give
-// 11.5 us with loading waves of their own. A few rows stream w: 1 row x 50280 x 2048 in
-// 40 us, 16 rows in 42 (206 MB, 4.9-5.1 TB/s).
+// takes 302-320 us, card to card (1080-1150 TFLOP/s; the library 335-360). At 256 x 2048 x
+// 4096 (one 64 x 32 tile per compute unit, one wave per SIMD, and as many that load) the
+// reads and MFMAs alone take 10.9 us of a stream of launches, the loads alone 10.2 (13.8
+// with w from memory), together 12.5 (14.5). A few rows stream w: 1 row x 50280 x 2048 in
+// 41 us, 16 rows in 42 (206 MB, 4.9-5.0 TB/s).
 #include <hip/hip_runtime.h>
 #include <math.h>
 #include <stdint.h>
@@ -180,7 +181,7 @@ constexpr int kChain = 512;
 // cores work on this one. NL waves issue
 // the loads; with APART waves of their own, where a compute unit has one small
 // tile and the issue of the loads would hold up its few MFMAs (256 x 2048 x 4096 in
-// 64 x 32 tiles: 15.5 us, 12.8 with eight loading waves, 11.6 with four apart).
+// 64 x 32 tiles: 15.8 us, 12.5 with four loading waves apart, 12.4 with eight).
 // LDS layout: row r of a tile at 2 BK r bytes, its 16-byte piece c at c ^ (r % 8),
 // so that the 16 rows that a fragment read touches spread over the banks. A
 // direct load fills 1 KB in lane order, whole rows or more, so a lane fetches
@@ -373,8 +374,8 @@ __device__ __forceinline__ void tile_steps(const char *buf, f32x4 (&acc)[C::FM][
 // eight row tiles or more, an XCD that takes every eighth tile sees an eighth of
 // the rows of x. With fewer, it takes a run of tiles instead, all rows of an
 // eighth of the columns, so that w, the larger operand then, goes to one XCD
-// (256 x 2048 x 4096 as 64 x 32 tiles: 15.4 against 20.7 us; 8192 x 8192 x 8192
-// the other way round: 950 against 990 us).
+// (256 x 2048 x 4096 as 64 x 32 tiles: 12.5 against 20.5 us; 8192 x 8192 x 8192
+// the other way round: 835 against 1000 us).
 __device__ __forceinline__ bool tile_of(int b, int mtiles, int ntiles, int &m, int &n) {
     const int t = mtiles < 8 ? (b & 7) * (int)(gridDim.x >> 3) + (b >> 3) : b;
     m = t % mtiles;

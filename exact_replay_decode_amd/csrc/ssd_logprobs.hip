@@ -382,8 +382,8 @@ void k_logprobs(LogprobArgs a) {
     __syncthreads();
 
     if (TOP && wave == 1) {
-        // (64 groups bound a small top_k well enough; the other waves wait here:
-        // 4 us of 98 for 4096 x 50280, top 5)
+        // (64 groups bound a small top_k well enough; the other waves wait here: uniform
+        // bf16 of 50280, top 8, 117 against 120 us for 4096 rows, 21.7 against 22.8 for 512)
         const float g = gm[2 * lane], h = gm[2 * lane + 1];
         const float tau = a.k <= 24 ? wave_kth(fmaxf(g, h), a.k) : wave_kth(g, h, a.k);
         if (lane == 0)

@@ -11,10 +11,11 @@
 // 32 KB, read once.
 // That plan is latency, not bytes: 512 slots of 16 pages take 5.9 us (the table's
 // one round trip beside the requests', the bits, two prefix sums, the search); with the
-// requests' rows read an entry at a time, and before the table, 8.7.
+// requests' rows read an entry at a time, and before the table, 8.7; 128 requests that
+// take 320 pages of a pool of 647, 7.0-7.7.
 // The copies move whole 16-byte pieces, eight loads in flight per thread
 // before the first store: 16 slots forked into 128 (272 MB written, 34 MB read) in
-// 53-59 us, 5.2-5.8 TB/s, where a fill of that size takes 40; 71 MB of pages moved in
+// 54-58 us, 5.3-5.7 TB/s, where a fill of that size takes 40; 71 MB of pages moved in
 // 23-25 us, 5.6-6.2 TB/s of both directions.
 #include <hip/hip_runtime.h>
 #include <stdint.h>

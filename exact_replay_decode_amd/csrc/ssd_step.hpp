@@ -62,8 +62,10 @@ constexpr int kLogprobStreams = 16, kLogprobChunk = 2048;
 // Waves of a row (16 or 4; the bits are the same). 16 while all rows run at the same time
 // (bf16 two to a compute unit: 512 rows of 50280 with top 8 in 18 against 24 us, 1024 in
 // 33 against 33, 2048 in 62 against 52; fp32 one: 256 rows in 14 against 18 us, 512 in 28
-// against 25), and in bf16 where every wave has four chunks or more (2048 rows of 131072
-// with top 8: 102 against 108 us) and the launch's threads, 64 a wave, fit 32 bits.
+// against 25), and in bf16 where every wave has four chunks or more and the launch's
+// threads, 64 a wave, fit 32 bits (16 waves against 4, 600 to 4096 rows, no or 8
+// alternatives, all or one token in 50 allowed: 0.66 to 1.01 of the time at 131072 to 262144
+// columns, 0.74 to 1.04 at 65536 to 114688, 0.85 to 1.24 at 50280).
 constexpr int logprob_waves(int64_t T, int32_t V, bool bf16) {
     if (T <= (bf16 ? 512 : 256))
         return 16;
