@@ -30,10 +30,10 @@
 
 #include <iterator>
 
-#include "ssd_device.hpp"
 #include "ssd_linear_choice.hpp"
 #include "ssd_step.h"
 #include "ssd_step.hpp"
+#include "ssd_step_device.hpp"
 
 namespace ssd {
 namespace {

@@ -16,8 +16,8 @@
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
-#include "ssd_device.hpp"
 #include "ssd_step.hpp"
+#include "ssd_step_device.hpp"
 
 namespace ssd {
 namespace {
