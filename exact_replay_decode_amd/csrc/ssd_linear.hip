@@ -6,10 +6,11 @@
 // 64-byte steps of k, ascending from zero: one v_mfma_f32_16x16x32_bf16 for the
 // step's 32 k in bf16, four v_mfma_f32_16x16x4_f32 for its 16 k in fp32 (the
 // i-th takes k = i, 4 + i, 8 + i, 12 + i of the step), where a chain ends after 512 k
-// and the chains are added in turn; k past K are zeros on both sides. An MFMA result element depends on its own row, its own column
-// and its accumulator only, so every tile shape here gives the same bits, and
-// a row's bits do not depend on the number of rows. (A wave has all of k: work comes
-// from outputs alone, and few of them with a long k take the time of their sum.)
+// and the chains are added in turn; k past K are zeros on both sides. An MFMA result
+// element depends on its own row, its own column and its accumulator only, so every tile
+// shape here gives the same bits, and a row's bits do not depend on the number of rows.
+// (A wave has all of k: work comes from outputs alone, and few of them with a long k
+// take the time of their sum.)
 //
 // The instruction's rows are output columns n and its columns are rows m of x:
 // a lane then holds four consecutive n of one row.
@@ -384,8 +385,8 @@ __device__ __forceinline__ bool tile_of(int b, int mtiles, int ntiles, int &m, i
 }
 
 template <class C>
-__global__ __launch_bounds__(64 * C::WAVES, C::PER_SIMD) void k_linear_tile(LinearArgs a, int mtiles,
-                                                             int ntiles) {
+__global__ __launch_bounds__(64 * C::WAVES, C::PER_SIMD)
+void k_linear_tile(LinearArgs a, int mtiles, int ntiles) {
     constexpr int S = C::S, BK = C::BK;
     __shared__ __attribute__((aligned(1024))) char buf[S * C::BYTES];
     const int wave = wave_id();

@@ -68,7 +68,7 @@ def _apart(outs, ins, same=()):
         a = t.data_ptr()
         b = a + t.nbytes
         for c, d, other in seen:
-            if a < d and c < b:
+            if a < d and c < b and a < b:
                 raise ValueError(f"{other} and {name} share memory")
         if a < b:
             seen.append((a, b, name))
